@@ -1,0 +1,413 @@
+"""The dense operators beside the virtual-noise layer, as they are measured: the linear layer with its epilogue
+and its backward pass, layer norm and its backward pass, and the AdamW step over many tensors.
+
+Together they are a training step of a pre-norm residual block around the centre of a population: the norm feeds
+the projection, the projection adds the residual, their gradients (or the estimated ones) feed the optimizer.
+``run`` computes a case in plain torch operations, or through ``virtual_noise_perturbed_amd`` where ``own`` is true.
+"""
+
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+BLOCK = 128                      # elements of 8-bit state that share a scale
+LR, BETA1, BETA2, EPS, DECAY = 1e-3, 0.9, 0.999, 1e-8, 0.01
+LN_EPS = 1e-5
+
+
+# ---------------------------------------------------------------------------
+# cases
+
+def _linear(name, rows, fin, fout, dtype, act, residual, op="linear"):
+    return {"name": name, "op": op, "rows": rows, "in": fin, "out": fout, "dtype": dtype, "act": act,
+            "residual": residual}
+
+
+def _norm(name, rows, width, dtype, op="layer_norm"):
+    return {"name": name, "op": op, "rows": rows, "width": width, "dtype": dtype}
+
+
+def _adamw(name, layers, width, bits, grads, copies):
+    return {"name": name, "op": "adamw", "layers": layers, "width": width, "bits": bits, "grads": grads,
+            "copies": copies}
+
+
+def listed():
+    return [
+        # one observation through the centre's 4096 -> 4096 projection while serving: latency and the weight's bytes
+        _linear("linear 1x4096x4096 bf16", 1, 4096, 4096, "bf16", "silu", True),
+        # the first layer of the 784-256-256-10 network on an odd batch, fp32
+        _linear("linear 2011x784x256 f32", 2011, 784, 256, "f32", "relu", False),
+        # the transformer-width projection on a training batch: bias, gelu and the residual in one call
+        _linear("linear 4096x4096x4096 bf16", 4096, 4096, 4096, "bf16", "gelu", True),
+        # the hidden layer's gradients, fp32, sizes off every tile
+        _linear("linear_backward 777x1024x1000 f32", 777, 1024, 1000, "f32", "gelu_tanh", False, "linear_backward"),
+        # the transformer-width projection's gradients: input, weight and bias
+        _linear("linear_backward 4096x4096x4096 bf16", 4096, 4096, 4096, "bf16", "gelu", False, "linear_backward"),
+        # one observation's norm while serving
+        _norm("layer_norm 1x512 f32", 1, 512, "f32"),
+        # every row of a population of 128 with 256 rows each
+        _norm("layer_norm 32768x4096 bf16", 32768, 4096, "bf16"),
+        # a narrow odd width, so that rows start at any address
+        _norm("layer_norm_backward 5003x1001 f32", 5003, 1001, "f32", "layer_norm_backward"),
+        _norm("layer_norm_backward 32768x4096 bf16", 32768, 4096, "bf16", "layer_norm_backward"),
+        # a policy of many small tensors: launches and the host's work
+        _adamw("adamw 12x4 tensors 63 wide", 12, 63, 32, "f32", False),
+        # four transformer-width blocks: fp32 centre, bf16 gradients and the bf16 copy that the layers read
+        _adamw("adamw 4 blocks 4096 wide", 4, 4096, 32, "bf16", True),
+        # the same blocks from the estimated fp32 gradient, with 8-bit states
+        _adamw("adamw 4 blocks 4096 wide 8-bit", 4, 4096, 8, "f32", False),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["linear", "linear_backward", "layer_norm", "layer_norm_backward", "adamw"])
+    dtype = rng.choice(["f32", "bf16"])
+    if op.startswith("linear"):
+        rows, fin, fout = _log_int(rng, 1, 8192), _log_int(rng, 16, 4096), _log_int(rng, 8, 4096)
+        if rng.random() < 0.5:       # half of the widths are whole vectors, as most layers' are
+            fin, fout = -(-fin // 64) * 64, -(-fout // 64) * 64
+        rows = min(rows, (1 << (33 if dtype == "f32" else 36)) // (fin * fout))
+        return {"op": op, "rows": rows, "in": fin, "out": fout, "dtype": dtype,
+                "act": rng.choice(["none", "relu", "gelu", "gelu_tanh", "silu"]),
+                "residual": op == "linear" and rng.random() < 0.5}
+    if op.startswith("layer_norm"):
+        width = _log_int(rng, 8, 16384)
+        if rng.random() < 0.5:
+            width = -(-width // 8) * 8
+        most = (1 << 27) // width // (2 if dtype == "f32" else 1)
+        return {"op": op, "rows": _log_int(rng, 1, min(most, 131072)), "width": width, "dtype": dtype}
+    layers, width = _log_int(rng, 1, 24), _log_int(rng, 16, 4096)
+    layers = max(1, min(layers, (1 << 26) // (width * width)))
+    return {"op": op, "layers": layers, "width": width, "bits": rng.choice([32, 8]), "grads": dtype,
+            "copies": rng.random() < 0.5}
+
+
+# ---------------------------------------------------------------------------
+# inputs
+
+def _tensor_shapes(case):
+    """Per block: the weight, its bias, and the norm's weight and bias."""
+    w = case["width"]
+    return [(w, w), (w,), (w,), (w,)] * case["layers"]
+
+
+def _layout(case):
+    """[(start, shape)] of each tensor in a flat buffer, starts at whole blocks, and the buffer's length."""
+    at, where = 0, []
+    for shape in _tensor_shapes(case):
+        where.append((at, shape))
+        at += -(-math.prod(shape) // BLOCK) * BLOCK
+    return where, at
+
+
+def _views(flat, where):
+    return [flat[at:at + math.prod(shape)].view(shape) for at, shape in where]
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+
+    def normal(*shape, scale=1.0, mean=0.0, dtype=torch.float32):
+        return (torch.randn(shape, generator=gen, device=dev) * scale + mean).to(dtype)
+
+    s = {"case": case}
+    if case["op"].startswith("linear"):
+        m, k, n, dt = case["rows"], case["in"], case["out"], DTYPES[case["dtype"]]
+        s["x"] = normal(m, k, dtype=dt)
+        s["w"] = normal(n, k, scale=k ** -0.5, dtype=dt)
+        s["b"] = normal(n, scale=0.1)
+        if case["op"] == "linear":
+            s["r"] = normal(m, n, dtype=dt) if case["residual"] else None
+        else:
+            s["dy"] = normal(m, n, dtype=dt)
+            s["pre"] = normal(m, n, dtype=dt) if case["act"] != "none" else None
+    elif case["op"].startswith("layer_norm"):
+        m, n, dt = case["rows"], case["width"], DTYPES[case["dtype"]]
+        s["x"] = normal(m, n, scale=2.0, mean=0.5, dtype=dt)
+        s["w"] = normal(n, scale=0.2, mean=1.0)
+        s["b"] = normal(n, scale=0.1)
+        if case["op"] == "layer_norm_backward":
+            s["dy"] = normal(m, n, dtype=dt)
+            var, mean = torch.var_mean(s["x"].float(), dim=1, correction=0)
+            s["mean"], s["rstd"] = mean, torch.rsqrt(var + LN_EPS)
+    else:
+        where, n = _layout(case)
+        used = torch.zeros(n, dtype=torch.bool, device=dev)
+        for v in _views(used, where):
+            v.fill_(True)
+        gdt = DTYPES[case["grads"]]
+        s["p"] = normal(n, scale=0.02) * used
+        s["g"] = (normal(n, scale=0.01) * used).to(gdt)
+        s["copy"] = torch.zeros(n, dtype=torch.bfloat16, device=dev) if case["copies"] else None
+        m, v = normal(n, scale=0.003) * used, normal(n, scale=0.01).square() * used
+        s["step"] = 10
+        s["state"] = {"exp_avg": m, "exp_avg_sq": v}
+        if case["bits"] == 8:
+            nb = n // BLOCK
+            # codes of a state in mid-training: every block's largest value at the format's top exponents
+            s["state"] = {"exp_avg": _to_fp8(m, 3, 7, -14, None), "exp_avg_sq": _to_fp8(v, 2, 15, -22, None),
+                          "exp_avg_scale": torch.full((nb,), 127 - 14, dtype=torch.uint8, device=dev),
+                          "exp_avg_sq_scale": torch.full((nb,), 127 - 22, dtype=torch.uint8, device=dev)}
+        s["params"], s["grads"] = _views(s["p"], where), _views(s["g"], where)
+        s["copies"] = _views(s["copy"], where) if case["copies"] else None
+        if own:
+            # the optimizer is a handle that a training program makes once, on its own parameter and gradient buffers
+            import virtual_noise_perturbed_amd as vn
+            s["opt"] = vn.AdamW(s["params"], s["grads"], lr=LR, betas=(BETA1, BETA2), eps=EPS, weight_decay=DECAY,
+                                copies=s["copies"], state_bits=case["bits"], state=dict(s["state"], step=s["step"]))
+    return s
+
+
+# ---------------------------------------------------------------------------
+# the plain forms
+
+def _phi(z):
+    return 0.5 * (1.0 + torch.erf(z * math.sqrt(0.5)))
+
+
+def _act(z, act):
+    if act == "relu":
+        return torch.where(z > 0, z, torch.zeros_like(z))
+    if act == "gelu":
+        return z * _phi(z)
+    if act == "gelu_tanh":
+        return 0.5 * z * (1.0 + torch.tanh(math.sqrt(2.0 / math.pi) * (z + 0.044715 * z * z * z)))
+    if act == "silu":
+        return z / (1.0 + torch.exp(-z))
+    return z
+
+
+def _act_slope(z, act):
+    if act == "relu":
+        return (z > 0).to(z.dtype)
+    if act == "gelu":
+        return _phi(z) + z * torch.exp(-0.5 * z * z) * (1.0 / math.sqrt(2.0 * math.pi))
+    if act == "gelu_tanh":
+        c = math.sqrt(2.0 / math.pi)
+        t = torch.tanh(c * (z + 0.044715 * z * z * z))
+        return 0.5 * (1.0 + t) + 0.5 * z * (1.0 - t * t) * c * (1.0 + 3 * 0.044715 * z * z)
+    if act == "silu":
+        g = 1.0 / (1.0 + torch.exp(-z))
+        return g * (1.0 + z * (1.0 - g))
+    return torch.ones_like(z)
+
+
+def _plain_linear(s):
+    c, dt = s["case"], s["x"].dtype
+    z = s["x"].float() @ s["w"].float().t() + s["b"]
+    y = _act(z, c["act"])
+    if s["r"] is not None:
+        y = y + s["r"].float()
+    return {"y": y.to(dt), "pre": z.to(dt)}
+
+
+def _plain_linear_backward(s):
+    c, dt = s["case"], s["x"].dtype
+    dz = s["dy"].float()
+    if c["act"] != "none":
+        dz = dz * _act_slope(s["pre"].float(), c["act"])
+    return {"dx": (dz @ s["w"].float()).to(dt), "dw": (dz.t() @ s["x"].float()).to(dt), "db": dz.sum(0)}
+
+
+def _plain_layer_norm(s):
+    x = s["x"].float()
+    mean = x.mean(1)
+    d = x - mean[:, None]
+    rstd = 1.0 / torch.sqrt((d * d).mean(1) + LN_EPS)
+    return {"y": (d * rstd[:, None] * s["w"] + s["b"]).to(s["x"].dtype), "mean": mean, "rstd": rstd}
+
+
+def _plain_layer_norm_backward(s):
+    dy = s["dy"].float()
+    xhat = (s["x"].float() - s["mean"][:, None]) * s["rstd"][:, None]
+    g = dy * s["w"]
+    dx = (g - g.mean(1)[:, None] - xhat * (g * xhat).mean(1)[:, None]) * s["rstd"][:, None]
+    return {"dx": dx.to(s["x"].dtype), "dw": (dy * xhat).sum(0), "db": dy.sum(0)}
+
+
+def _exponent(x):
+    """The biased exponent field of fp32 values."""
+    return (x.abs().view(torch.int32) >> 23).to(torch.int32)
+
+
+def _pow2(biased):
+    return (biased << 23).view(torch.float32)
+
+
+def _from_fp8(codes, scale):
+    return (codes.float().view(-1, BLOCK) * _pow2(scale.to(torch.int32))[:, None]).view(-1)
+
+
+def _to_fp8(x, mant, bias, log2_scale, theta):
+    """fp8 codes (``mant`` mantissa bits, exponent bias ``bias``) of x / 2^log2_scale (a number, or a tensor for each
+    element); ``theta`` in [0, 1) is each element's rounding offset (None: nearest).  Positive values of the
+    unsigned state (e5m2) keep at least the smallest code."""
+    if isinstance(log2_scale, int):
+        a = x.abs() * 2.0 ** -log2_scale
+    else:
+        a = x.abs() * _pow2(127 - log2_scale)
+    e = torch.clamp(_exponent(a) - 127 + bias, min=1)
+    q = torch.floor(a * _pow2(127 - (e - bias) + mant) + (0.5 if theta is None else theta))
+    code = ((e - 1) << mant) + q.to(torch.int32)
+    if mant == 2:
+        code = torch.where((x > 0) & (code == 0), torch.ones_like(code), code)
+    code = torch.where(x < 0, code + 128, code).to(torch.uint8)
+    return code.view(torch.float8_e4m3fn if mant == 3 else torch.float8_e5m2)
+
+
+def _block_exponent(x, top):
+    """The scale's biased exponent of each block: the largest magnitude lands at exponent ``top``."""
+    return torch.clamp(_exponent(x.abs().view(-1, BLOCK).amax(1)) - top, min=1)
+
+
+def _per_element(v):
+    return v[:, None].expand(-1, BLOCK).reshape(-1)
+
+
+def _plain_adamw(s):
+    c, st = s["case"], s["state"]
+    s["step"] += 1
+    t = s["step"]
+    g = s["g"].float()
+    if c["bits"] == 8:
+        m, v = _from_fp8(st["exp_avg"], st["exp_avg_scale"]), _from_fp8(st["exp_avg_sq"], st["exp_avg_sq_scale"])
+    else:
+        m, v = st["exp_avg"], st["exp_avg_sq"]
+    m = m * BETA1 + g * (1.0 - BETA1)
+    v = v * BETA2 + (g * g) * (1.0 - BETA2)
+    denom = torch.sqrt(v) * (1.0 / math.sqrt(1.0 - BETA2 ** t)) + EPS
+    p = s["p"] * (1.0 - LR * DECAY) - (m / denom) * (LR / (1.0 - BETA1 ** t))
+    s["p"].copy_(p)
+    if c["copies"]:
+        s["copy"].copy_(p)
+    if c["bits"] == 8:
+        at = torch.arange(m.numel(), device=m.device)
+        theta = (((t * 0x9E3779B9 + at * 0xC13FA9A9) & 0xFFFFFFFF) >> 8).float() * 2.0 ** -24
+        em, ev = _block_exponent(m, 7), _block_exponent(v, 14)
+        st["exp_avg"].copy_(_to_fp8(m, 3, 7, _per_element(em) - 127, theta))
+        st["exp_avg_sq"].copy_(_to_fp8(v, 2, 15, _per_element(ev) - 127, theta))
+        st["exp_avg_scale"].copy_(em)
+        st["exp_avg_sq_scale"].copy_(ev)
+    else:
+        st["exp_avg"].copy_(m)
+        st["exp_avg_sq"].copy_(v)
+    return _adamw_outputs(s)
+
+
+def _adamw_outputs(s):
+    out = dict(s["state"], p=s["p"])
+    if s["copy"] is not None:
+        out["copy"] = s["copy"]
+    return out
+
+
+# ---------------------------------------------------------------------------
+# one pass
+
+def run(state):
+    s = state
+    c = s["case"]
+    if not own:
+        return {"linear": _plain_linear, "linear_backward": _plain_linear_backward, "layer_norm": _plain_layer_norm,
+                "layer_norm_backward": _plain_layer_norm_backward, "adamw": _plain_adamw}[c["op"]](s)
+    import virtual_noise_perturbed_amd as vn
+    if c["op"] == "linear":
+        pre = torch.empty((c["rows"], c["out"]), dtype=s["x"].dtype, device=s["x"].device)
+        y = vn.linear(s["x"], s["w"], s["b"], activation=c["act"], residual=s["r"], pre=pre)
+        return {"y": y, "pre": pre}
+    if c["op"] == "linear_backward":
+        dx, dw, db = vn.linear_backward(s["dy"], s["x"], s["w"], activation=c["act"], pre=s["pre"])
+        return {"dx": dx, "dw": dw, "db": db}
+    if c["op"] == "layer_norm":
+        y, mean, rstd = vn.layer_norm(s["x"], s["w"], s["b"], eps=LN_EPS, stats=True)
+        return {"y": y, "mean": mean, "rstd": rstd}
+    if c["op"] == "layer_norm_backward":
+        dx, dw, db = vn.layer_norm_backward(s["dy"], s["x"], s["mean"], s["rstd"], s["w"])
+        return {"dx": dx, "dw": dw, "db": db}
+    s["opt"].step()
+    return _adamw_outputs(s)
+
+
+def work(case):
+    if case["op"].startswith("linear"):
+        m, k, n = case["rows"], case["in"], case["out"]
+        e = 2 if case["dtype"] == "bf16" else 4
+        if case["op"] == "linear":
+            return {"bytes": e * (m * k + n * k + m * n * (3 if case["residual"] else 2)) + 4 * n, "flops": 2.0 * m * n * k}
+        return {"bytes": e * (2 * m * k + 2 * n * k + m * n * (1 if case["act"] == "none" else 2)) + 4 * n,
+                "flops": 4.0 * m * n * k}
+    if case["op"].startswith("layer_norm"):
+        m, n = case["rows"], case["width"]
+        e = 2 if case["dtype"] == "bf16" else 4
+        if case["op"] == "layer_norm":
+            return {"bytes": 2 * e * m * n + 8 * m + 8 * n, "flops": 8.0 * m * n}
+        return {"bytes": 3 * e * m * n + 8 * m + 12 * n, "flops": 14.0 * m * n}
+    n = sum(math.prod(s) for s in _tensor_shapes(case))
+    per = 8 + (2 if case["grads"] == "bf16" else 4) + (16 if case["bits"] == 32 else 4) + (2 if case["copies"] else 0)
+    return {"bytes": float(per * n) + (4 * n / BLOCK if case["bits"] == 8 else 0), "flops": 16.0 * n}
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    d = {k: v.double() for k, v in s.items() if isinstance(v, torch.Tensor) and "float8" not in str(v.dtype)}
+    if case["op"] == "linear":
+        z = torch.addmm(d["b"], d["x"], d["w"].t())
+        y = {"none": lambda: z, "relu": lambda: z.clamp(min=0), "silu": lambda: z * torch.sigmoid(z),
+             "gelu": lambda: torch.special.ndtr(z) * z,
+             "gelu_tanh": lambda: z * torch.sigmoid(2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3))}[case["act"]]()
+        return {"y": y + d["r"] if case["residual"] else y, "pre": z}
+    if case["op"] == "linear_backward":
+        dz = d["dy"]
+        if case["act"] != "none":
+            z = d["pre"]
+            if case["act"] == "relu":
+                slope = torch.heaviside(z, torch.zeros((), dtype=z.dtype, device=z.device))
+            elif case["act"] == "gelu":
+                slope = torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+            else:   # z times a sigmoid of u(z)
+                a = 2 * math.sqrt(2 / math.pi) if case["act"] == "gelu_tanh" else 1.0
+                q = 0.044715 if case["act"] == "gelu_tanh" else 0.0
+                g = torch.sigmoid(a * (z + q * z ** 3))
+                slope = g + z * g * (1 - g) * a * (1 + 3 * q * z ** 2)
+            dz = dz * slope
+        return {"dx": torch.mm(dz, d["w"]), "dw": torch.mm(dz.t().contiguous(), d["x"]), "db": dz.sum(0)}
+    if case["op"] == "layer_norm":
+        var, mean = torch.var_mean(d["x"], dim=1, correction=0)
+        rstd = (var + LN_EPS).rsqrt()
+        return {"y": (d["x"] - mean[:, None]).mul_(rstd[:, None]).mul_(d["w"]).add_(d["b"]), "mean": mean, "rstd": rstd}
+    if case["op"] == "layer_norm_backward":
+        xhat = d["x"].sub_(d["mean"][:, None]).mul_(d["rstd"][:, None])
+        g = d["dy"] * d["w"]
+        a, b = g.mean(1, keepdim=True), (g * xhat).mean(1, keepdim=True)
+        return {"dx": g.sub_(a).sub_(xhat * b).mul_(d["rstd"][:, None]), "dw": (d["dy"] * xhat).sum(0), "db": d["dy"].sum(0)}
+    st, t, small = s["state"], s["step"] + 1, case["bits"] == 8
+
+    def held(name):
+        if not small:
+            return st[name].double()
+        scale = torch.exp2(st[name + "_scale"].double() - 127).repeat_interleave(BLOCK)
+        return st[name].to(torch.float64) * scale
+
+    m = BETA1 * held("exp_avg") + (1 - BETA1) * d["g"]
+    v = BETA2 * held("exp_avg_sq") + (1 - BETA2) * d["g"] ** 2
+    p = d["p"] - LR * DECAY * d["p"] - LR * (m / (1 - BETA1 ** t)) / ((v / (1 - BETA2 ** t)).sqrt() + EPS)
+    out = {"exp_avg": m, "exp_avg_sq": v, "p": p}
+    if small:
+        # the codes depend on the rounding offsets as well as on the values; the scales are whole numbers
+        out.update(exp_avg=None, exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None)
+    if case["copies"]:
+        out["copy"] = p
+    return out
