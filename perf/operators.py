@@ -292,7 +292,7 @@ def _plain_adamw(s):
         s["copy"].copy_(p)
     if c["bits"] == 8:
         at = torch.arange(m.numel(), device=m.device)
-        theta = (((t * 0x9E3779B9 + at * 0xC13FA9A9) & 0xFFFFFFFF) >> 8).float() * 2.0 ** -24
+        theta = (((t * 0x9E3779B9 + at * 0xC13FA9A9) & 0xFFFFFFFF) >> 12).float() * 2.0 ** -20
         em, ev = _block_exponent(m, 7), _block_exponent(v, 14)
         st["exp_avg"].copy_(_to_fp8(m, 3, 7, _per_element(em) - 127, theta))
         st["exp_avg_sq"].copy_(_to_fp8(v, 2, 15, _per_element(ev) - 127, theta))
