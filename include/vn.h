@@ -53,7 +53,7 @@
 extern "C" {
 #endif
 
-#define VN_ABI_VERSION 3
+#define VN_ABI_VERSION 4
 
 typedef enum vn_status {
   VN_OK = 0,
@@ -80,7 +80,11 @@ typedef enum vn_index_dtype {
 
 typedef enum vn_activation {
   VN_ACT_NONE = 0,      /* Y as defined above                                            */
-  VN_ACT_RELU = 1       /* max(Y, 0) applied in the same kernel (for chaining layers)    */
+  VN_ACT_RELU = 1,      /* max(Y, 0) applied in the same kernel (for chaining layers)    */
+  /* the dense layer alone (vn_linear, vn_linear_backward): */
+  VN_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2                                   */
+  VN_ACT_SILU = 3,      /* z / (1 + exp(-z))                                             */
+  VN_ACT_GELU_TANH = 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2               */
 } vn_activation;
 
 typedef enum vn_math {
@@ -286,6 +290,153 @@ int vn_noise_u32(const void* seeds, int32_t seed_dtype, int64_t pop, int64_t n, 
                  uint32_t* r_out, void* stream);
 int vn_noise_f32(const void* seeds, int32_t seed_dtype, int64_t pop, int64_t n, int64_t offset,
                  float* n_out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Dense operators: the training and evaluation of the centre that a population
+ * is spread around.  The same conventions hold; floating point operands are
+ * VN_F32 or VN_BF16 as their vn_dtype arguments say, biases, norm weights and
+ * statistics are fp32, and sums are held in fp32.
+ */
+
+/*
+ * Linear layer with its epilogue:
+ *   z = x W^T + b,   y = act(z) + residual
+ *   x          (rows, in) and w (out, in), both in `dtype`, 16-byte aligned
+ *   bias       (out,) fp32, or NULL
+ *   residual   (rows, out) in `out_dtype`, or NULL; may be y itself
+ *   activation any vn_activation
+ *   y          (rows, out) in `out_dtype`
+ *   pre        (rows, out) in `dtype`, or NULL: receives z, for vn_linear_backward
+ *   workspace  DEVICE scratch of workspace_bytes >= vn_linear_workspace_size,
+ *              16-byte aligned (may be NULL when that is 0); its contents on
+ *              entry do not matter, and calls that share it must be ordered by
+ *              the caller
+ * VN_BF16: bf16 products, fp32 accumulation, one rounding to the outputs.
+ * VN_F32: products of the operands split into three bf16 values each (what is
+ * dropped is below 2^-24 of a product), fp32 accumulation; up to 16 rows
+ * multiply in fp32.  A non-finite fp32 input makes the outputs it reaches
+ * non-finite (an infinity may come out as NaN).
+ * in == 0 gives z = b.  Errors: VN_ERR_NULL, VN_ERR_SHAPE (negative size,
+ * workspace too small), VN_ERR_VALUE (activation), VN_ERR_DTYPE,
+ * VN_ERR_OVERFLOW (a size product, or 2^31 and more tiles of 64 x 64),
+ * VN_ERR_ALIGN (x, w or workspace not 16-byte aligned, another pointer not
+ * aligned to its element).
+ */
+int vn_linear(const void* x, const void* w, int32_t dtype, const float* bias, const void* residual,
+              int64_t rows, int64_t in, int64_t out, int32_t activation, int32_t out_dtype, void* y, void* pre,
+              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device workspace, in bytes, that vn_linear needs for these sizes. */
+int vn_linear_workspace_size(int32_t dtype, int64_t rows, int64_t in, int64_t out, int64_t* bytes_out);
+
+/*
+ * Gradients of vn_linear:
+ *   dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum over rows of dz
+ * (the residual's gradient is dy itself).
+ *   dy         (rows, out) in `dy_dtype`, 16-byte aligned
+ *   x, w       as in vn_linear
+ *   pre        (rows, out) in `dtype`: the z that vn_linear stored; unused (may
+ *              be NULL) for VN_ACT_NONE
+ *   dx         (rows, in) in `dtype`, or NULL when not wanted
+ *   dw         (out, in) in `dw_dtype`, or NULL
+ *   db         (out,) fp32, or NULL
+ *   workspace  as in vn_linear, vn_linear_backward_workspace_size bytes for the
+ *              same sizes and the same outputs wanted
+ * For VN_BF16, dz is rounded to bf16 before the two products; db is summed
+ * from the unrounded dz.  rows == 0 gives dw = 0 and db = 0.  Errors as in
+ * vn_linear.
+ */
+int vn_linear_backward(const void* dy, int32_t dy_dtype, const void* x, const void* w, int32_t dtype,
+                       const void* pre, int64_t rows, int64_t in, int64_t out, int32_t activation,
+                       void* dx, void* dw, int32_t dw_dtype, float* db,
+                       void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device workspace, in bytes, that vn_linear_backward needs; wanted: 1 dx, 2 dw, 4 db, or-ed. */
+int vn_linear_backward_workspace_size(int32_t dtype, int32_t dy_dtype, int64_t rows, int64_t in, int64_t out,
+                                      int32_t activation, int32_t wanted, int64_t* bytes_out);
+
+/*
+ * Layer norm over the last axis:
+ *   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+ *   y = (x - mean) rstd weight + bias
+ *   x          (rows, n) in x_dtype;  y (rows, n) in y_dtype (y may be x when the types agree)
+ *   weight     (n,) fp32 or NULL (ones);  bias (n,) fp32 or NULL (zeros)
+ *   eps        finite, >= 0
+ *   mean, rstd (rows,) fp32 or NULL: the statistics, for the backward pass
+ * Errors also: VN_ERR_SHAPE for n == 0 with rows > 0 (the mean of nothing is
+ * undefined), VN_ERR_VALUE (eps), VN_ERR_OVERFLOW (rows * n).
+ */
+int vn_layer_norm(const void* x, int32_t x_dtype, const float* weight, const float* bias, int64_t rows, int64_t n,
+                  float eps, void* y, int32_t y_dtype, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of vn_layer_norm, xhat = (x - mean) rstd, g = dy weight:
+ *   dx      = rstd (g - sum g / n - xhat sum (g xhat) / n)     (rows, n) in x_dtype, or NULL
+ *   dweight = sum over rows of dy xhat                         (n,) fp32, or NULL
+ *   dbias   = sum over rows of dy                              (n,) fp32, or NULL
+ *   dy         (rows, n) in dy_dtype (dx may be dy or x when the types agree)
+ *   mean, rstd as vn_layer_norm gave them
+ *   workspace  DEVICE scratch of workspace_bytes >= vn_layer_norm_backward_workspace_size
+ *              (partial column sums; may be NULL when neither dweight nor dbias
+ *              is wanted); 16-byte aligned
+ * rows == 0 gives dweight = 0 and dbias = 0.  Errors as in vn_layer_norm.
+ */
+int vn_layer_norm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const float* weight,
+                           const float* mean, const float* rstd, int64_t rows, int64_t n,
+                           void* dx, float* dweight, float* dbias,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device workspace, in bytes, that vn_layer_norm_backward needs for its column sums. */
+int vn_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int64_t* bytes_out);
+
+/*
+ * One AdamW step over many tensors, t the step's number (from 1):
+ *   m <- beta1 m + (1 - beta1) g        v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, with g negated first when `maximize` is not 0.
+ *   n_tensors, and HOST arrays of n_tensors entries:
+ *     numel          elements of each tensor (0 allowed)
+ *     params         DEVICE pointers, param_dtypes each (VN_F32, or VN_BF16: the
+ *                    new value is rounded to nearest even)
+ *     grads          DEVICE pointers, grad_dtypes each
+ *     copies         DEVICE pointers to a bf16 copy of the new value or NULL
+ *                    entries; NULL = none at all
+ *     weight_decay   of each tensor
+ *     state_offsets  first state element of each tensor: multiples of 128, and
+ *                    each tensor's elements, rounded up to 128, within state_len
+ *                    and apart from the others'
+ *   state_bits       32: exp_avg and exp_avg_sq are (state_len,) fp32
+ *                    8:  (state_len,) fp8 codes, e4m3 and e5m2, with one scale
+ *                    for every 128 of them in exp_avg_scale / exp_avg_sq_scale
+ *                    ((state_len / 128,) uint8 e: a code stands for its value
+ *                    times 2^(e - 127)).  Codes are rounded up when the
+ *                    fraction and the offset ((t 0x9E3779B9 + i 0xC13FA9A9 mod
+ *                    2^32) >> 12) 2^-20 of state element i reach 1, so that
+ *                    averages move by less than a code's width; a positive v is
+ *                    never 0.  Where a block's m or v is not finite, its scale is 255 and all
+ *                    of the block stands for infinities.
+ *                    exp_avg and exp_avg_sq are 16-byte aligned.  Elements that
+ *                    pad a tensor to 128 are kept 0.
+ *   step, lr, beta1, beta2, eps   t >= 1; lr, eps >= 0; betas in [0, 1)
+ *   coefficients     DEVICE, or NULL: what vn_adamw_coefficients wrote, used
+ *                    in place of `step` and of lr's part in the update (lr
+ *                    still sets the weight decay)
+ * 64 tensors go in one launch.  Errors: VN_ERR_NULL, VN_ERR_SHAPE, VN_ERR_VALUE,
+ * VN_ERR_DTYPE, VN_ERR_ALIGN, VN_ERR_OVERFLOW.
+ */
+int vn_adamw_step(int32_t n_tensors, const int64_t* numel, void* const* params, const int32_t* param_dtypes,
+                  const void* const* grads, const int32_t* grad_dtypes, void* const* copies,
+                  const double* weight_decay, const int64_t* state_offsets, int64_t state_len, int32_t state_bits,
+                  void* exp_avg, void* exp_avg_sq, uint8_t* exp_avg_scale, uint8_t* exp_avg_sq_scale,
+                  int64_t step, double lr, double beta1, double beta2, double eps, int32_t maximize,
+                  const void* coefficients, void* stream);
+
+/*
+ * Counts a step on the device, for steps captured into a graph: *step += 1,
+ * and the coefficients of that step for vn_adamw_step.
+ *   step          DEVICE int64;  coefficients DEVICE, 16 bytes, 16-byte aligned
+ */
+int vn_adamw_coefficients(int64_t* step, double lr, double beta1, double beta2, void* coefficients, void* stream);
 
 #ifdef __cplusplus
 }

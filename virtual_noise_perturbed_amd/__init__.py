@@ -31,6 +31,11 @@ __all__ = [
     "virtual_reduce_metric_noalloc",
     "noise_u32",
     "noise_f32",
+    "linear",
+    "linear_backward",
+    "layer_norm",
+    "layer_norm_backward",
+    "AdamW",
     "VNError",
 ]
 
@@ -377,3 +382,7 @@ def noise_f32(seeds: torch.Tensor, n: int, offset: int) -> torch.Tensor:
     st = lib.vn_noise_f32(_ptr(s), kind, s.shape[0], int(n), int(offset), _ptr(r), _stream(s.device))
     _lib.check("vn_noise_f32", st)
     return r
+
+
+# The dense operators check and marshal with the helpers above.
+from .dense import AdamW, layer_norm, layer_norm_backward, linear, linear_backward  # noqa: E402

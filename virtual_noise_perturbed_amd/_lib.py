@@ -8,14 +8,14 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_float, c_int32, c_int64, c_void_p
+from ctypes import c_double, c_float, c_int32, c_int64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libvn.so")
 
 VN_OK, VN_ERR_NULL, VN_ERR_SHAPE, VN_ERR_VALUE, VN_ERR_DTYPE, VN_ERR_OVERFLOW, VN_ERR_HIP, VN_ERR_ALIGN = range(8)
 VN_F32, VN_BF16 = 0, 1
 VN_I64, VN_I32 = 0, 1
-VN_ACT_NONE, VN_ACT_RELU = 0, 1
+VN_ACT_NONE, VN_ACT_RELU, VN_ACT_GELU, VN_ACT_SILU, VN_ACT_GELU_TANH = range(5)
 VN_MATH_DEFAULT, VN_MATH_F32 = 0, 1
 
 # name -> argument types, in the order of include/vn.h
@@ -43,6 +43,21 @@ SIGNATURES = {
                                  c_void_p, c_void_p],
     "vn_noise_u32": [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p],
     "vn_noise_f32": [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_void_p],
+    "vn_linear": [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int32, c_int32,
+                  c_void_p, c_void_p, c_void_p, c_int64, c_void_p],
+    "vn_linear_workspace_size": [c_int32, c_int64, c_int64, c_int64, c_void_p],
+    "vn_linear_backward": [c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_int64, c_int64, c_int64,
+                           c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_void_p],
+    "vn_linear_backward_workspace_size": [c_int32, c_int32, c_int64, c_int64, c_int64, c_int32, c_int32, c_void_p],
+    "vn_layer_norm": [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_float, c_void_p, c_int32,
+                      c_void_p, c_void_p, c_void_p],
+    "vn_layer_norm_backward": [c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_int64,
+                               c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p],
+    "vn_layer_norm_backward_workspace_size": [c_int64, c_int64, c_void_p],
+    "vn_adamw_step": [c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                      c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_double, c_double,
+                      c_double, c_double, c_int32, c_void_p, c_void_p],
+    "vn_adamw_coefficients": [c_void_p, c_double, c_double, c_double, c_void_p, c_void_p],
 }
 
 _RESTYPES = {"vn_status_string": ctypes.c_char_p, "vn_last_hip_error": ctypes.c_char_p}

@@ -1,6 +1,7 @@
 // C ABI of the virtual-noise ES linear layer: argument validation and launch
 // selection.  Every check runs before any HIP call; the kernels themselves are
-// in vn_kernels.hip.  Declarations and the contract are in include/vn.h.
+// in vn_kernels.hip and vn_gemm.hip; the dense operators' entry points are in
+// vn_dense_api.cpp.  Declarations and the contract are in include/vn.h.
 
 #include "vn.h"
 
@@ -11,6 +12,7 @@
 #include <cstring>
 #include <limits>
 
+#include "vn_dense.hpp"
 #include "vn_launch.hpp"
 
 namespace {
@@ -38,13 +40,6 @@ int seed_kind(int32_t seed_dtype, bool* is_i32) {
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return VN_OK;
-  std::strncpy(g_last_hip_error, hipGetErrorString(e), sizeof(g_last_hip_error) - 1);
-  g_last_hip_error[sizeof(g_last_hip_error) - 1] = '\0';
-  return VN_ERR_HIP;
-}
-
 // Shared checks of the gradient-style entry points over n flat elements.
 int check_gradient(const float* fitness, const void* seeds, int32_t seed_dtype, int64_t pop_size, int64_t n,
                    float sigma, int64_t offset, const void* out, bool* i32, float* scale) {
@@ -66,6 +61,17 @@ int check_gradient(const float* fitness, const void* seeds, int32_t seed_dtype, 
 }
 
 }  // namespace
+
+namespace vn {
+int hip_status(hipError_t e) {
+  if (e == hipSuccess) return VN_OK;
+  std::strncpy(g_last_hip_error, hipGetErrorString(e), sizeof(g_last_hip_error) - 1);
+  g_last_hip_error[sizeof(g_last_hip_error) - 1] = '\0';
+  return VN_ERR_HIP;
+}
+}  // namespace vn
+
+using vn::hip_status;
 
 extern "C" {
 

@@ -1,0 +1,140 @@
+// Internal launch interface between the C ABI of the dense operators
+// (vn_dense_api.cpp) and their kernels (vn_norm.hip, vn_adamw.hip,
+// vn_linear.hip).  Arguments reaching these functions are already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace vn {
+
+// Element type of a dense operand.
+enum class Elem : int32_t { f32 = 0, bf16 = 1 };
+
+// hipError_t -> vn_status, keeping the error's text for vn_last_hip_error (vn_api.cpp).
+int hip_status(hipError_t e);
+
+// ---- layer norm (vn_norm.hip) ----------------------------------------------
+
+struct NormParams {
+  const void* x;         // (rows, n)
+  Elem x_type;
+  const float* weight;   // (n,) or null (ones)
+  const float* bias;     // (n,) or null (zeros)
+  int64_t rows, n;       // both > 0
+  float eps;
+  void* y;               // (rows, n)
+  Elem y_type;
+  float* mean;           // (rows,) or null
+  float* rstd;           // (rows,) or null
+};
+hipError_t launch_layer_norm(const NormParams& p, hipStream_t stream);
+
+struct NormBackwardParams {
+  const void* dy;        // (rows, n)
+  Elem dy_type;
+  const void* x;         // (rows, n); dx has its type
+  Elem x_type;
+  const float* weight;   // (n,) or null (ones)
+  const float* mean;     // (rows,)
+  const float* rstd;     // (rows,)
+  int64_t rows, n;       // n > 0
+  void* dx;              // (rows, n) or null
+  float* dweight;        // (n,) or null
+  float* dbias;          // (n,) or null
+  float* partial;        // workspace
+};
+// Bytes of workspace the backward pass uses for its partial column sums.
+int64_t layer_norm_backward_workspace(int64_t rows, int64_t n);
+hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t stream);
+
+// first[c] = sum of partial[k * pitch + c] over k < parts, and, when it is not
+// null, second[c] = sum of partial[k * pitch + n + c], in a fixed order.
+hipError_t launch_join_columns(const float* partial, int64_t parts, int64_t pitch, int64_t n, float* first,
+                               float* second, hipStream_t stream);
+
+// ---- AdamW (vn_adamw.hip) --------------------------------------------------
+
+constexpr int kAdamBlock = 128;         // elements of 8-bit state that share a scale
+constexpr int kAdamTensors = 64;        // tensors per launch (their table travels as a kernel argument)
+
+struct AdamTensor {
+  void* p;
+  const void* g;
+  __bf16* copy;          // bf16 copy of an fp32 parameter, or null
+  int64_t n;             // elements
+  int64_t state;         // first element of its state
+  uint32_t first_chunk;  // first workgroup-chunk of the launch that is this tensor's
+  float decay;           // 1 - lr * weight decay
+  uint32_t flags;        // bit 0: p is bf16; bit 1: g is bf16
+  uint32_t pad;
+};
+
+// Coefficients of one step, on the host or (vn_adamw_coefficients) on the device.
+struct AdamCoef {
+  float step_size;       // lr / (1 - beta1^t)
+  float inv_root;        // 1 / sqrt(1 - beta2^t)
+  uint32_t dither;       // t * 0x9E3779B9 mod 2^32
+  uint32_t pad;
+};
+
+struct AdamParams {
+  void* m;
+  void* v;
+  uint8_t* m_scale;      // 8-bit states
+  uint8_t* v_scale;
+  const AdamCoef* coef_dev;  // or null: coef
+  AdamCoef coef;
+  float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float sign;            // -1 to ascend
+  int32_t tensors;
+  uint32_t chunks;       // workgroups of the launch
+  AdamTensor t[kAdamTensors];
+};
+constexpr int64_t kAdamChunk = 4096;    // elements per workgroup
+hipError_t launch_adamw(const AdamParams& p, int bits, hipStream_t stream);
+hipError_t launch_adamw_coefficients(int64_t* step, double lr, double beta1, double beta2, AdamCoef* coef,
+                                     hipStream_t stream);
+
+
+// ---- linear layer (vn_linear.hip) ------------------------------------------
+
+enum class Act : int32_t { none = 0, relu = 1, gelu = 2, silu = 3, gelu_tanh = 4 };
+
+struct LinearParams {
+  const void* x;         // (rows, in)
+  const void* w;         // (out, in), x's type
+  Elem type;
+  const float* bias;     // (out,) or null
+  const void* residual;  // (rows, out) in out_type, or null
+  int64_t rows, in, out;
+  Act act;
+  Elem out_type;
+  void* y;               // (rows, out)
+  void* pre;             // (rows, out) in type, or null: x W^T + b
+  char* workspace;
+};
+// rows and out > 0.
+int64_t linear_workspace(Elem type, int64_t rows, int64_t in, int64_t out);
+hipError_t launch_linear(const LinearParams& p, hipStream_t stream);
+
+struct LinearBackwardParams {
+  const void* dy;        // (rows, out)
+  Elem dy_type;
+  const void* x;         // (rows, in)
+  const void* w;         // (out, in)
+  Elem type;             // of x, w, pre and dx
+  const void* pre;       // (rows, out); unused without an activation
+  int64_t rows, in, out;
+  Act act;
+  void* dx;              // (rows, in) or null
+  void* dw;              // (out, in) in dw_type, or null
+  Elem dw_type;
+  float* db;             // (out,) or null
+  char* workspace;
+};
+int64_t linear_backward_workspace(Elem type, Elem dy_type, Act act, int64_t rows, int64_t in, int64_t out, bool dx,
+                                  bool dw, bool db);
+hipError_t launch_linear_backward(const LinearBackwardParams& p, hipStream_t stream);
+
+}  // namespace vn

@@ -1,0 +1,315 @@
+// C ABI of the dense operators (linear layer, layer norm, AdamW): argument
+// validation and launch.  Every check runs before any HIP call.  Declarations
+// and the contract are in include/vn.h.
+
+#include "vn.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <limits>
+
+#include "vn_dense.hpp"
+
+namespace {
+
+constexpr int64_t kI64Max = std::numeric_limits<int64_t>::max();
+
+bool mul_ok(int64_t a, int64_t b, int64_t* r) {  // a, b >= 0
+  if (a != 0 && b > kI64Max / a) return false;
+  *r = a * b;
+  return true;
+}
+
+bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+bool elem(int32_t dtype, vn::Elem* e) {
+  if (dtype == VN_F32) *e = vn::Elem::f32;
+  else if (dtype == VN_BF16) *e = vn::Elem::bf16;
+  else return false;
+  return true;
+}
+size_t size_of(vn::Elem e) { return e == vn::Elem::f32 ? 4 : 2; }
+
+bool act_of(int32_t activation, vn::Act* a) {
+  switch (activation) {
+    case VN_ACT_NONE: *a = vn::Act::none; return true;
+    case VN_ACT_RELU: *a = vn::Act::relu; return true;
+    case VN_ACT_GELU: *a = vn::Act::gelu; return true;
+    case VN_ACT_SILU: *a = vn::Act::silu; return true;
+    case VN_ACT_GELU_TANH: *a = vn::Act::gelu_tanh; return true;
+    default: return false;
+  }
+}
+
+// Sizes of a linear layer: the three matrices' bytes with three bf16 planes,
+// 64-padding and split partial sums in int64, and tile counts in 31 bits.
+int check_linear_sizes(int64_t rows, int64_t in, int64_t out) {
+  if (rows < 0 || in < 0 || out < 0) return VN_ERR_SHAPE;
+  constexpr int64_t kMost = int64_t{1} << 31;
+  if (rows >= kMost || in >= kMost || out >= kMost) return VN_ERR_OVERFLOW;
+  const int64_t d[3] = {(rows + 63) / 64, (in + 63) / 64, (out + 63) / 64};
+  for (int i = 0; i < 3; ++i)
+    if (d[i] * d[(i + 1) % 3] >= kMost) return VN_ERR_OVERFLOW;
+  return VN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int vn_linear_workspace_size(int32_t dtype, int64_t rows, int64_t in, int64_t out, int64_t* bytes_out) {
+  vn::Elem t;
+  if (bytes_out == nullptr) return VN_ERR_NULL;
+  if (!elem(dtype, &t)) return VN_ERR_DTYPE;
+  const int st = check_linear_sizes(rows, in, out);
+  if (st != VN_OK) return st;
+  *bytes_out = rows == 0 || out == 0 ? 0 : vn::linear_workspace(t, rows, in, out);
+  return VN_OK;
+}
+
+int vn_linear(const void* x, const void* w, int32_t dtype, const float* bias, const void* residual, int64_t rows,
+              int64_t in, int64_t out, int32_t activation, int32_t out_dtype, void* y, void* pre, void* workspace,
+              int64_t workspace_bytes, void* stream) {
+  vn::LinearParams p;
+  if (!elem(dtype, &p.type) || !elem(out_dtype, &p.out_type)) return VN_ERR_DTYPE;
+  const int st = check_linear_sizes(rows, in, out);
+  if (st != VN_OK) return st;
+  if (!act_of(activation, &p.act)) return VN_ERR_VALUE;
+  if (workspace_bytes < 0) return VN_ERR_SHAPE;
+  if (rows == 0 || out == 0) return VN_OK;
+  if (y == nullptr || (in > 0 && (x == nullptr || w == nullptr))) return VN_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 16) || !aligned(bias, 4) ||
+      !aligned(y, size_of(p.out_type)) || !aligned(residual, size_of(p.out_type)) || !aligned(pre, size_of(p.type)))
+    return VN_ERR_ALIGN;
+  const int64_t need = vn::linear_workspace(p.type, rows, in, out);
+  if (need > 0 && workspace == nullptr) return VN_ERR_NULL;
+  if (workspace_bytes < need) return VN_ERR_SHAPE;
+  p.x = x;
+  p.w = w;
+  p.bias = bias;
+  p.residual = residual;
+  p.rows = rows;
+  p.in = in;
+  p.out = out;
+  p.y = y;
+  p.pre = pre;
+  p.workspace = static_cast<char*>(workspace);
+  return vn::hip_status(vn::launch_linear(p, static_cast<hipStream_t>(stream)));
+}
+
+int vn_linear_backward_workspace_size(int32_t dtype, int32_t dy_dtype, int64_t rows, int64_t in, int64_t out,
+                                      int32_t activation, int32_t wanted, int64_t* bytes_out) {
+  vn::Elem t, g;
+  vn::Act a;
+  if (bytes_out == nullptr) return VN_ERR_NULL;
+  if (!elem(dtype, &t) || !elem(dy_dtype, &g)) return VN_ERR_DTYPE;
+  const int st = check_linear_sizes(rows, in, out);
+  if (st != VN_OK) return st;
+  if (!act_of(activation, &a) || wanted < 0 || wanted > 7) return VN_ERR_VALUE;
+  *bytes_out = vn::linear_backward_workspace(t, g, a, rows, in, out, (wanted & 1) != 0, (wanted & 2) != 0,
+                                             (wanted & 4) != 0);
+  return VN_OK;
+}
+
+int vn_linear_backward(const void* dy, int32_t dy_dtype, const void* x, const void* w, int32_t dtype, const void* pre,
+                       int64_t rows, int64_t in, int64_t out, int32_t activation, void* dx, void* dw,
+                       int32_t dw_dtype, float* db, void* workspace, int64_t workspace_bytes, void* stream) {
+  vn::LinearBackwardParams p;
+  if (!elem(dtype, &p.type) || !elem(dy_dtype, &p.dy_type) || !elem(dw_dtype, &p.dw_type)) return VN_ERR_DTYPE;
+  const int st = check_linear_sizes(rows, in, out);
+  if (st != VN_OK) return st;
+  if (!act_of(activation, &p.act)) return VN_ERR_VALUE;
+  if (workspace_bytes < 0) return VN_ERR_SHAPE;
+  if (rows * out > 0 && (dy == nullptr || (p.act != vn::Act::none && pre == nullptr))) return VN_ERR_NULL;
+  if (out * in > 0 && dx != nullptr && rows > 0 && w == nullptr) return VN_ERR_NULL;
+  if (rows * in > 0 && dw != nullptr && out > 0 && x == nullptr) return VN_ERR_NULL;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(workspace, 16) ||
+      !aligned(pre, size_of(p.type)) || !aligned(dx, size_of(p.type)) || !aligned(dw, size_of(p.dw_type)) ||
+      !aligned(db, 4))
+    return VN_ERR_ALIGN;
+  const int64_t need = vn::linear_backward_workspace(p.type, p.dy_type, p.act, rows, in, out, dx != nullptr,
+                                                     dw != nullptr, db != nullptr);
+  if (need > 0 && workspace == nullptr) return VN_ERR_NULL;
+  if (workspace_bytes < need) return VN_ERR_SHAPE;
+  p.dy = dy;
+  p.x = x;
+  p.w = w;
+  p.pre = pre;
+  p.rows = rows;
+  p.in = in;
+  p.out = out;
+  p.dx = dx;
+  p.dw = dw;
+  p.db = db;
+  p.workspace = static_cast<char*>(workspace);
+  return vn::hip_status(vn::launch_linear_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+int vn_layer_norm(const void* x, int32_t x_dtype, const float* weight, const float* bias, int64_t rows, int64_t n,
+                  float eps, void* y, int32_t y_dtype, float* mean, float* rstd, void* stream) {
+  vn::NormParams p;
+  if (!elem(x_dtype, &p.x_type) || !elem(y_dtype, &p.y_type)) return VN_ERR_DTYPE;
+  if (rows < 0 || n < 0) return VN_ERR_SHAPE;
+  int64_t total;
+  if (!mul_ok(rows, n, &total) || !mul_ok(total, 4, &total)) return VN_ERR_OVERFLOW;
+  if (!std::isfinite(eps) || eps < 0.0f) return VN_ERR_VALUE;
+  if (rows == 0) return VN_OK;
+  if (n == 0) return VN_ERR_SHAPE;  // the mean of nothing is undefined
+  if (x == nullptr || y == nullptr) return VN_ERR_NULL;
+  if (!aligned(x, size_of(p.x_type)) || !aligned(y, size_of(p.y_type)) || !aligned(weight, 4) || !aligned(bias, 4) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return VN_ERR_ALIGN;
+  p.x = x;
+  p.weight = weight;
+  p.bias = bias;
+  p.rows = rows;
+  p.n = n;
+  p.eps = eps;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  return vn::hip_status(vn::launch_layer_norm(p, static_cast<hipStream_t>(stream)));
+}
+
+int vn_layer_norm_backward_workspace_size(int64_t rows, int64_t n, int64_t* bytes_out) {
+  if (bytes_out == nullptr) return VN_ERR_NULL;
+  if (rows < 0 || n < 0) return VN_ERR_SHAPE;
+  int64_t total;
+  if (!mul_ok(rows, n, &total) || !mul_ok(n, 8192, &total)) return VN_ERR_OVERFLOW;
+  *bytes_out = vn::layer_norm_backward_workspace(rows, n);
+  return VN_OK;
+}
+
+int vn_layer_norm_backward(const void* dy, int32_t dy_dtype, const void* x, int32_t x_dtype, const float* weight,
+                           const float* mean, const float* rstd, int64_t rows, int64_t n, void* dx, float* dweight,
+                           float* dbias, void* workspace, int64_t workspace_bytes, void* stream) {
+  vn::NormBackwardParams p;
+  if (!elem(dy_dtype, &p.dy_type) || !elem(x_dtype, &p.x_type)) return VN_ERR_DTYPE;
+  if (rows < 0 || n < 0 || workspace_bytes < 0) return VN_ERR_SHAPE;
+  int64_t total;
+  if (!mul_ok(rows, n, &total) || !mul_ok(total, 4, &total) || !mul_ok(n, 8192, &total)) return VN_ERR_OVERFLOW;
+  if (rows == 0 && n == 0) return VN_OK;
+  if (n == 0) return VN_ERR_SHAPE;  // the mean of nothing is undefined
+  if (rows > 0 && (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr)) return VN_ERR_NULL;
+  if (!aligned(dy, size_of(p.dy_type)) || !aligned(x, size_of(p.x_type)) || !aligned(dx, size_of(p.x_type)) ||
+      !aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) || !aligned(dbias, 4) ||
+      !aligned(workspace, 16))
+    return VN_ERR_ALIGN;
+  if (dweight != nullptr || dbias != nullptr) {
+    const int64_t need = vn::layer_norm_backward_workspace(rows, n);
+    if (need > 0 && workspace == nullptr) return VN_ERR_NULL;
+    if (workspace_bytes < need) return VN_ERR_SHAPE;
+  }
+  p.dy = dy;
+  p.x = x;
+  p.weight = weight;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.n = n;
+  p.dx = dx;
+  p.dweight = dweight;
+  p.dbias = dbias;
+  p.partial = static_cast<float*>(workspace);
+  return vn::hip_status(vn::launch_layer_norm_backward(p, static_cast<hipStream_t>(stream)));
+}
+
+int vn_adamw_step(int32_t n_tensors, const int64_t* numel, void* const* params, const int32_t* param_dtypes,
+                  const void* const* grads, const int32_t* grad_dtypes, void* const* copies,
+                  const double* weight_decay, const int64_t* state_offsets, int64_t state_len, int32_t state_bits,
+                  void* exp_avg, void* exp_avg_sq, uint8_t* exp_avg_scale, uint8_t* exp_avg_sq_scale, int64_t step,
+                  double lr, double beta1, double beta2, double eps, int32_t maximize, const void* coefficients,
+                  void* stream) {
+  if (n_tensors < 0 || state_len < 0) return VN_ERR_SHAPE;
+  if (state_bits != 32 && state_bits != 8) return VN_ERR_VALUE;
+  if (state_len % vn::kAdamBlock != 0) return VN_ERR_SHAPE;
+  if (!std::isfinite(lr) || lr < 0.0 || !std::isfinite(eps) || eps < 0.0) return VN_ERR_VALUE;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return VN_ERR_VALUE;
+  if (coefficients == nullptr && step < 1) return VN_ERR_VALUE;
+  if (n_tensors == 0) return VN_OK;
+  if (numel == nullptr || params == nullptr || param_dtypes == nullptr || grads == nullptr || grad_dtypes == nullptr ||
+      weight_decay == nullptr || state_offsets == nullptr)
+    return VN_ERR_NULL;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < n_tensors; ++i) {
+    vn::Elem pt, gt;
+    if (!elem(param_dtypes[i], &pt) || !elem(grad_dtypes[i], &gt)) return VN_ERR_DTYPE;
+    if (numel[i] < 0) return VN_ERR_SHAPE;
+    if (!std::isfinite(weight_decay[i])) return VN_ERR_VALUE;
+    const void* copy = copies != nullptr ? copies[i] : nullptr;
+    if (copy != nullptr && pt != vn::Elem::f32) return VN_ERR_DTYPE;
+    if (numel[i] == 0) continue;
+    if (numel[i] > state_len) return VN_ERR_SHAPE;
+    const int64_t padded = (numel[i] + vn::kAdamBlock - 1) / vn::kAdamBlock * vn::kAdamBlock;
+    if (state_offsets[i] < 0 || state_offsets[i] % vn::kAdamBlock != 0 || state_offsets[i] > state_len - padded)
+      return VN_ERR_SHAPE;
+    if (params[i] == nullptr || grads[i] == nullptr) return VN_ERR_NULL;
+    if (!aligned(params[i], size_of(pt)) || !aligned(grads[i], size_of(gt)) || !aligned(copy, 2)) return VN_ERR_ALIGN;
+    const int64_t c = (numel[i] + vn::kAdamChunk - 1) / vn::kAdamChunk;
+    if (c > 0x7FFFFFFF) return VN_ERR_OVERFLOW;
+    chunks += c;
+  }
+  if (chunks == 0) return VN_OK;
+  if (exp_avg == nullptr || exp_avg_sq == nullptr) return VN_ERR_NULL;
+  if (!aligned(exp_avg, 16) || !aligned(exp_avg_sq, 16)) return VN_ERR_ALIGN;
+  if (state_bits == 8 && (exp_avg_scale == nullptr || exp_avg_sq_scale == nullptr)) return VN_ERR_NULL;
+  if (!aligned(coefficients, 16)) return VN_ERR_ALIGN;
+
+  vn::AdamParams a;
+  a.m = exp_avg;
+  a.v = exp_avg_sq;
+  a.m_scale = exp_avg_scale;
+  a.v_scale = exp_avg_sq_scale;
+  a.coef_dev = static_cast<const vn::AdamCoef*>(coefficients);
+  a.coef = {};
+  if (coefficients == nullptr) {
+    const double t = static_cast<double>(step);
+    a.coef.step_size = static_cast<float>(lr / (1.0 - std::pow(beta1, t)));
+    a.coef.inv_root = static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+    a.coef.dither = static_cast<uint32_t>(step) * 0x9E3779B9u;
+  }
+  a.beta1 = static_cast<float>(beta1);
+  a.one_minus_beta1 = static_cast<float>(1.0 - beta1);
+  a.beta2 = static_cast<float>(beta2);
+  a.one_minus_beta2 = static_cast<float>(1.0 - beta2);
+  a.eps = static_cast<float>(eps);
+  a.sign = maximize != 0 ? -1.0f : 1.0f;
+  a.tensors = 0;
+  a.chunks = 0;
+  hipError_t err = hipSuccess;
+  for (int32_t i = 0; i <= n_tensors && err == hipSuccess; ++i) {
+    const int64_t c = i < n_tensors ? (numel[i] + vn::kAdamChunk - 1) / vn::kAdamChunk : 0;
+    if (a.tensors > 0 && (i == n_tensors || a.tensors == vn::kAdamTensors || a.chunks + c > 0x7FFFFFFF)) {
+      err = vn::launch_adamw(a, state_bits, static_cast<hipStream_t>(stream));
+      a.tensors = 0;
+      a.chunks = 0;
+    }
+    if (c == 0) continue;
+    vn::AdamTensor& t = a.t[a.tensors++];
+    t.p = params[i];
+    t.g = grads[i];
+    t.copy = copies != nullptr ? static_cast<__bf16*>(copies[i]) : nullptr;
+    t.n = numel[i];
+    t.state = state_offsets[i];
+    t.first_chunk = a.chunks;
+    t.decay = static_cast<float>(1.0 - lr * weight_decay[i]);
+    t.flags = (param_dtypes[i] == VN_BF16 ? 1u : 0u) | (grad_dtypes[i] == VN_BF16 ? 2u : 0u);
+    t.pad = 0;
+    a.chunks += static_cast<uint32_t>(c);
+  }
+  return vn::hip_status(err);
+}
+
+int vn_adamw_coefficients(int64_t* step, double lr, double beta1, double beta2, void* coefficients, void* stream) {
+  if (!std::isfinite(lr) || lr < 0.0) return VN_ERR_VALUE;
+  if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return VN_ERR_VALUE;
+  if (step == nullptr || coefficients == nullptr) return VN_ERR_NULL;
+  if (!aligned(step, 8) || !aligned(coefficients, 16)) return VN_ERR_ALIGN;
+  return vn::hip_status(vn::launch_adamw_coefficients(step, lr, beta1, beta2,
+                                                      static_cast<vn::AdamCoef*>(coefficients),
+                                                      static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,538 @@
+// Layer norm over the last axis and its gradients (gfx950).
+//   mean = sum x / n,  rstd = 1 / sqrt(sum (x - mean)^2 / n + eps)
+//   y    = (x - mean) rstd w + b
+//   g    = dy w,  xhat = (x - mean) rstd
+//   dx   = rstd (g - sum g / n - xhat sum (g xhat) / n)
+//   dw   = sum over rows of dy xhat,  db = sum over rows of dy
+// Everything between the loads and the stores is fp32; the variance is summed
+// from the differences to the mean (the row is in registers by then), never
+// as E[x^2] - mean^2.  Sums are divided by n, not multiplied by its inverse: the
+// mean of a constant row is the constant.
+//
+// What bounds it: the bytes of x, dy, y and dx, each touched once.  A row of
+// up to 16384 (backward: 8192) is held in registers by G lanes, NV runs of 8 elements a lane;
+// the lanes keep their columns from row to row, so the weights are loaded once
+// per workgroup and a backward pass's column sums stay in registers until the
+// workgroup has walked all its rows (blockIdx.x, + gridDim.x, ...).  The next
+// row's loads are issued before the current row's sums are formed.
+#include <type_traits>
+
+#include "vn_dense.hpp"
+#include "vn_rows.hpp"
+
+namespace vn {
+namespace {
+
+constexpr int64_t kMaxResident = 16384;   // longest row held in registers (forward; half of it backward)
+
+// Sum of v over the G lanes of a row; G > 64 spans waves of the workgroup and
+// goes through `red` (two slots of G / 64 values, alternated by the caller so
+// that one barrier per sum is enough).
+template <int G>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  if constexpr (G <= 64) {
+    return group_sum<G>(v);
+  } else {
+    constexpr int W = G / 64;
+    v = group_sum<64>(v);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += red[w];
+    return s;
+  }
+}
+// Two sums at once.
+template <int G>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
+  if constexpr (G <= 64) {
+    a = group_sum<G>(a);
+    b = group_sum<G>(b);
+  } else {
+    constexpr int W = G / 64;
+    a = group_sum<64>(a);
+    b = group_sum<64>(b);
+    if ((threadIdx.x & 63) == 0) {
+      red[threadIdx.x >> 6] = a;
+      red[W + (threadIdx.x >> 6)] = b;
+    }
+    __syncthreads();
+    a = 0.0f;
+    b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      a += red[w];
+      b += red[W + w];
+    }
+  }
+}
+
+template <int G> constexpr int block_threads() { return G > 256 ? G : 256; }
+
+template <typename XT, typename YT, int G, int NV>
+__global__ __launch_bounds__(block_threads<G>()) void norm_kernel(NormParams p) {
+  constexpr int ROWS = block_threads<G>() / G;
+  __shared__ float red[G > 64 ? 4 * (G / 64) : 1];
+  const int lane = threadIdx.x % G;
+  const int n = static_cast<int>(p.n);
+  const float count = static_cast<float>(n);
+  const XT* __restrict__ x = static_cast<const XT*>(p.x);
+  YT* __restrict__ y = static_cast<YT*>(p.y);
+  float w[NV][8], b[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = (j * G + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[j][i] = 1.0f;
+      b[j][i] = 0.0f;
+    }
+    if (p.weight != nullptr) run_values(load_run(p.weight, c, n), w[j]);
+    if (p.bias != nullptr) run_values(load_run(p.bias, c, n), b[j]);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+  int64_t r = r0 + threadIdx.x / G;
+  Run8<XT> next[NV];
+  auto fetch = [&](int64_t row) {
+    // rows past the end are read from the last row and not stored
+    const XT* xr = x + (row < p.rows ? row : p.rows - 1) * n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) next[j] = load_run(xr, (j * G + lane) * 8, n);
+  };
+  fetch(r);
+  // every lane of the workgroup takes the same number of turns (barriers)
+  for (int64_t base = r0; base < p.rows; base += step, r += step) {
+    Run8<XT> cur[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) cur[j] = next[j];
+    if (base + step < p.rows) fetch(r + step);
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float v[8];
+      run_values(cur[j], v);
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    const float mean = row_sum<G>(s, red) / count;
+    float q = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + lane) * 8;
+      float v[8];
+      run_values(cur[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = c + i < n ? v[i] - mean : 0.0f;
+        q += d * d;
+      }
+    }
+    const float var = row_sum<G>(q, red + (G > 64 ? G / 64 : 0)) / count;
+    const float rstd = 1.0f / sqrtf(var + p.eps);
+    if (r < p.rows) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * G + lane) * 8;
+        float v[8];
+        run_values(cur[j], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * rstd * w[j][i] + b[j][i];
+        if (c < n) store_run(y + r * n, c, n, v);
+      }
+      if (lane == 0) {
+        if (p.mean != nullptr) p.mean[r] = mean;
+        if (p.rstd != nullptr) p.rstd[r] = rstd;
+      }
+    }
+  }
+}
+
+// Rows longer than the registers hold: one workgroup of 1024 walks the row
+// three times (sum, squared differences, output); the second and third walk
+// find it in the caches.
+template <typename XT, typename YT>
+__global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
+  __shared__ float red[32];
+  const int64_t n = p.n;
+  const float count = static_cast<float>(n);
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const XT* xr = static_cast<const XT*>(p.x) + r * n;
+    YT* yr = static_cast<YT*>(p.y) + r * n;
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+      float v[8];
+      run_values(load_run(xr, c, n), v);
+      s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    }
+    const float mean = row_sum<1024>(s, red) / count;
+    float q = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+      float v[8];
+      run_values(load_run(xr, c, n), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = c + i < n ? v[i] - mean : 0.0f;
+        q += d * d;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<1024>(q, red + 16) / count + p.eps);
+    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+      float v[8], w[8], b[8];
+      run_values(load_run(xr, c, n), v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = 1.0f;
+        b[i] = 0.0f;
+      }
+      if (p.weight != nullptr) run_values(load_run(p.weight, c, n), w);
+      if (p.bias != nullptr) run_values(load_run(p.bias, c, n), b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * rstd * w[i] + b[i];
+      store_run(yr, c, n, v);
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean != nullptr) p.mean[r] = mean;
+      if (p.rstd != nullptr) p.rstd[r] = rstd;
+    }
+  }
+}
+
+// Gradients.  Column sums of the rows a workgroup walked go to
+// partial[blockIdx.x][2][n] (dw, then db), added in workgroup order by
+// join_columns_kernel: the same bits on every call.
+template <typename GT, typename XT, int G, int NV>
+__global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormBackwardParams p) {
+  constexpr int T = block_threads<G>();
+  constexpr int ROWS = T / G;
+  __shared__ float red[G > 64 ? 4 * (G / 64) : 1];
+  __shared__ float join[ROWS > 1 ? T * NV * 8 : 1];
+  const int lane = threadIdx.x % G;
+  const int n = static_cast<int>(p.n);
+  const float count = static_cast<float>(n);
+  const GT* __restrict__ dy = static_cast<const GT*>(p.dy);
+  const XT* __restrict__ x = static_cast<const XT*>(p.x);
+  XT* __restrict__ dx = static_cast<XT*>(p.dx);
+  float w[NV][8], sw[NV][8], sb[NV][8];
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      w[j][i] = 1.0f;
+      sw[j][i] = 0.0f;
+      sb[j][i] = 0.0f;
+    }
+    if (p.weight != nullptr) run_values(load_run(p.weight, (j * G + lane) * 8, n), w[j]);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * ROWS;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * ROWS;
+  int64_t r = r0 + threadIdx.x / G;
+  Run8<XT> nx[NV];
+  Run8<GT> ng[NV];
+  float nmean = 0.0f, nrstd = 0.0f;
+  auto fetch = [&](int64_t row) {
+    // rows past the end are read from the last row; they add nothing below
+    const int64_t q = row < p.rows ? row : p.rows - 1;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + lane) * 8;
+      nx[j] = load_run(x + q * n, c, n);
+      ng[j] = load_run(dy + q * n, c, n);
+    }
+    nmean = p.mean[q];
+    nrstd = p.rstd[q];
+  };
+  if (r0 < p.rows) fetch(r);
+  int par = 0;
+  for (int64_t base = r0; base < p.rows; base += step, r += step) {
+    Run8<XT> cx[NV];
+    Run8<GT> cg[NV];
+    const float mean = nmean, rstd = nrstd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      cx[j] = nx[j];
+      cg[j] = ng[j];
+    }
+    if (base + step < p.rows) fetch(r + step);
+    const bool valid = r < p.rows;
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + lane) * 8;
+      float xv[8], gv[8];
+      run_values(cx[j], xv);
+      run_values(cg[j], gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // (columns past n hold dy = 0; their x - mean is not formed, so that an
+        // infinite statistic there cannot turn a zero into NaN)
+        const float h = c + i < n ? (xv[i] - mean) * rstd : 0.0f;
+        const float t = gv[i] * h, g = gv[i] * w[j][i];
+        if (valid) {
+          sw[j][i] += t;
+          sb[j][i] += gv[i];
+        }
+        a += g;
+        b += g * h;
+      }
+    }
+    row_sum2<G>(a, b, red + (G > 64 ? par * 2 * (G / 64) : 0));
+    par ^= 1;
+    a /= count;
+    b /= count;
+    if (valid && dx != nullptr) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * G + lane) * 8;
+        float xv[8], gv[8];
+        run_values(cx[j], xv);
+        run_values(cg[j], gv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) xv[i] = rstd * (gv[i] * w[j][i] - a - (xv[i] - mean) * rstd * b);
+        if (c < n) store_run(dx + r * n, c, n, xv);
+      }
+    }
+  }
+  if (p.dweight == nullptr && p.dbias == nullptr) return;
+  // Several rows side by side: their sums join in row order.
+  auto join_rows = [&](float (&s)[NV][8]) {
+    if constexpr (ROWS > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) join[(j * 8 + i) * T + threadIdx.x] = s[j][i];
+      __syncthreads();
+      if (threadIdx.x < G) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float t = 0.0f;
+            for (int k = 0; k < ROWS; ++k) t += join[(j * 8 + i) * T + k * G + threadIdx.x];
+            s[j][i] = t;
+          }
+      }
+    }
+  };
+  join_rows(sw);
+  join_rows(sb);
+  if (threadIdx.x < G) {
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * n;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * G + lane) * 8;
+      if (c < n) {
+        store_run(out, c, n, sw[j]);
+        store_run(out + n, c, n, sb[j]);
+      }
+    }
+  }
+}
+
+// Rows longer than the registers hold: dx by one workgroup per row, in two
+// walks; the column sums by column_sums_kernel.
+template <typename GT, typename XT>
+__global__ __launch_bounds__(1024) void norm_backward_long_kernel(NormBackwardParams p) {
+  __shared__ float red[64];
+  const int64_t n = p.n;
+  const float count = static_cast<float>(n);
+  int par = 0;
+  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
+    const XT* xr = static_cast<const XT*>(p.x) + r * n;
+    const GT* gr = static_cast<const GT*>(p.dy) + r * n;
+    XT* dr = static_cast<XT*>(p.dx) + r * n;
+    const float mean = p.mean[r], rstd = p.rstd[r];
+    float a = 0.0f, b = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+      float xv[8], gv[8], w[8];
+      run_values(load_run(xr, c, n), xv);
+      run_values(load_run(gr, c, n), gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+      if (p.weight != nullptr) run_values(load_run(p.weight, c, n), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float h = c + i < n ? (xv[i] - mean) * rstd : 0.0f;
+        a += gv[i] * w[i];
+        b += gv[i] * w[i] * h;
+      }
+    }
+    row_sum2<1024>(a, b, red + par * 32);
+    par ^= 1;
+    a /= count;
+    b /= count;
+    for (int64_t c = threadIdx.x * 8; c < n; c += 8192) {
+      float xv[8], gv[8], w[8];
+      run_values(load_run(xr, c, n), xv);
+      run_values(load_run(gr, c, n), gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+      if (p.weight != nullptr) run_values(load_run(p.weight, c, n), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xv[i] = rstd * (gv[i] * w[i] - a - (xv[i] - mean) * rstd * b);
+      store_run(dr, c, n, xv);
+    }
+  }
+}
+
+// Column sums over the rows blockIdx.y, + gridDim.y, ... of 2048 columns
+// (8 per lane), into partial[blockIdx.y].
+template <typename GT, typename XT>
+__global__ __launch_bounds__(256) void column_sums_kernel(NormBackwardParams p) {
+  const int64_t n = p.n;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (c >= n) return;
+  float sw[8] = {}, sb[8] = {};
+  for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
+    float xv[8], gv[8];
+    run_values(load_run(static_cast<const XT*>(p.x) + r * n, c, n), xv);
+    run_values(load_run(static_cast<const GT*>(p.dy) + r * n, c, n), gv);
+    const float mean = p.mean[r], rstd = p.rstd[r];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sw[i] += gv[i] * ((xv[i] - mean) * rstd);
+      sb[i] += gv[i];
+    }
+  }
+  float* out = p.partial + static_cast<int64_t>(blockIdx.y) * 2 * n;
+  store_run(out, c, n, sw);
+  store_run(out + n, c, n, sb);
+}
+
+// Sums of partial rows in a fixed order: 64 columns by 4 waves, each a quarter
+// of the rows, joined in wave order.  Blocks of grid.y 1 take the second sum,
+// n further on in each partial row.
+__global__ __launch_bounds__(256) void join_columns_kernel(const float* partial, int64_t parts, int64_t pitch,
+                                                           int64_t n, float* first, float* second) {
+  __shared__ float s[256];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  float* out = blockIdx.y == 0 ? first : second;
+  if (out == nullptr) return;
+  float t = 0.0f;
+  if (c < n) {
+    const int64_t per = (parts + 3) / 4;
+    const int64_t end = (wave + 1) * per < parts ? (wave + 1) * per : parts;
+    const float* src = partial + blockIdx.y * n + c;
+    for (int64_t k = wave * per; k < end; ++k) t += src[k * pitch];
+  }
+  s[threadIdx.x] = t;
+  __syncthreads();
+  if (wave == 0 && c < n) out[c] = ((s[lane] + s[lane + 64]) + s[lane + 128]) + s[lane + 192];
+}
+
+// The layout of a row over lanes: G lanes of NV runs each.
+struct RowShape {
+  int g, nv;
+};
+RowShape row_shape(int64_t n, bool backward) {
+  if (n <= 128) return {16, 1};
+  if (n <= 512) return {64, 1};
+  if (n <= 1024) return {64, 2};
+  if (n <= 2048) return {256, 1};
+  if (n <= 4096) return {256, 2};
+  if (n <= 8192) return {512, 2};
+  // (a backward lane also holds the column sums and two rows: 16 waves have no registers for that)
+  if (n <= kMaxResident && !backward) return {1024, 2};
+  return {0, 0};
+}
+
+// f(G, NV) with the row shape's values as compile-time constants.
+template <bool BACKWARD, typename F>
+hipError_t with_shape(RowShape s, F&& f) {
+#define VN_SHAPE(G_, NV_) \
+  if (s.g == G_ && s.nv == NV_) return f(std::integral_constant<int, G_>{}, std::integral_constant<int, NV_>{});
+  VN_SHAPE(16, 1)
+  VN_SHAPE(64, 1)
+  VN_SHAPE(64, 2)
+  VN_SHAPE(256, 1)
+  VN_SHAPE(256, 2)
+  VN_SHAPE(512, 2)
+  if constexpr (!BACKWARD) {
+    VN_SHAPE(1024, 2)
+  }
+#undef VN_SHAPE
+  return hipErrorInvalidValue;
+}
+
+template <typename F>
+hipError_t with_types(Elem a, Elem b, F&& f) {
+  if (a == Elem::f32) return b == Elem::f32 ? f(float{}, float{}) : f(float{}, __bf16{});
+  return b == Elem::f32 ? f(__bf16{}, float{}) : f(__bf16{}, __bf16{});
+}
+
+constexpr int64_t kNormGrid = 2048;       // workgroups of 256: 8 per CU
+constexpr int64_t kBackwardGrid = 512;    // 2 per CU: their partial sums are written and read once more
+
+int64_t backward_parts(int64_t rows, int64_t n) {
+  const RowShape s = row_shape(n, true);
+  if (s.g == 0) return rows < 64 ? rows : 64;
+  const int64_t per = s.g > 256 ? 1 : 256 / s.g;
+  const int64_t blocks = (rows + per - 1) / per;
+  return blocks < kBackwardGrid ? blocks : kBackwardGrid;
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const NormParams& p, hipStream_t stream) {
+  const RowShape s = row_shape(p.n, false);
+  return with_types(p.x_type, p.y_type, [&](auto xt, auto yt) -> hipError_t {
+    using XT = decltype(xt);
+    using YT = decltype(yt);
+    if (s.g == 0) {
+      norm_long_kernel<XT, YT><<<static_cast<unsigned>(p.rows < kNormGrid ? p.rows : kNormGrid), 1024, 0, stream>>>(p);
+      return hipGetLastError();
+    }
+    return with_shape<false>(s, [&](auto g, auto nv) -> hipError_t {
+      constexpr int T = block_threads<decltype(g)::value>();
+      const int64_t per = T / g.value;
+      const int64_t blocks = (p.rows + per - 1) / per;
+      const int64_t most = kNormGrid * 256 / T;
+      norm_kernel<XT, YT, decltype(g)::value, decltype(nv)::value>
+          <<<static_cast<unsigned>(blocks < most ? blocks : most), T, 0, stream>>>(p);
+      return hipGetLastError();
+    });
+  });
+}
+
+int64_t layer_norm_backward_workspace(int64_t rows, int64_t n) {
+  return backward_parts(rows, n) * 2 * n * static_cast<int64_t>(sizeof(float));
+}
+
+hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t stream) {
+  const RowShape s = row_shape(p.n, true);
+  const int64_t parts = backward_parts(p.rows, p.n);
+  const bool sums = p.dweight != nullptr || p.dbias != nullptr;
+  if (parts > 0) {
+    const hipError_t e = with_types(p.dy_type, p.x_type, [&](auto gt, auto xt) -> hipError_t {
+      using GT = decltype(gt);
+      using XT = decltype(xt);
+      if (s.g == 0) {
+        if (p.dx != nullptr)
+          norm_backward_long_kernel<GT, XT>
+              <<<static_cast<unsigned>(p.rows < kNormGrid ? p.rows : kNormGrid), 1024, 0, stream>>>(p);
+        if (sums)
+          column_sums_kernel<GT, XT><<<dim3(static_cast<unsigned>((p.n + 2047) / 2048), static_cast<unsigned>(parts)),
+                                       256, 0, stream>>>(p);
+        return hipGetLastError();
+      }
+      return with_shape<true>(s, [&](auto g, auto nv) -> hipError_t {
+        norm_backward_kernel<GT, XT, decltype(g)::value, decltype(nv)::value>
+            <<<static_cast<unsigned>(parts), block_threads<decltype(g)::value>(), 0, stream>>>(p);
+        return hipGetLastError();
+      });
+    });
+    if (e != hipSuccess) return e;
+  }
+  return sums ? launch_join_columns(p.partial, parts, 2 * p.n, p.n, p.dweight, p.dbias, stream) : hipSuccess;
+}
+
+hipError_t launch_join_columns(const float* partial, int64_t parts, int64_t pitch, int64_t n, float* first,
+                               float* second, hipStream_t stream) {
+  join_columns_kernel<<<dim3(static_cast<unsigned>((n + 63) / 64), second != nullptr ? 2 : 1), 256, 0, stream>>>(
+      partial, parts, pitch, n, first, second);
+  return hipGetLastError();
+}
+
+}  // namespace vn

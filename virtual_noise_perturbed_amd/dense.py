@@ -1,0 +1,399 @@
+"""Dense operators beside the virtual-noise layer: the linear layer with its
+epilogue, layer norm, the gradients of both, and the AdamW step.
+
+They train and evaluate the centre that a population is spread around: the
+gradient comes from ``linear_backward`` / ``layer_norm_backward`` or from the
+evolution-strategies estimators, and goes to ``AdamW``.  As everywhere in the
+binding, each call only checks and marshals its arguments and runs in the HIP
+kernels of ``libvn.so``, asynchronously on the current stream.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Dict, List, Optional, Sequence, Tuple, Union
+
+import torch
+
+from . import _lib, _ptr, _require_device, _stream
+
+_ELEM = {torch.float32: _lib.VN_F32, torch.bfloat16: _lib.VN_BF16}
+_ACTIVATIONS = {None: _lib.VN_ACT_NONE, "none": _lib.VN_ACT_NONE, "relu": _lib.VN_ACT_RELU,
+                "gelu": _lib.VN_ACT_GELU, "silu": _lib.VN_ACT_SILU, "gelu_tanh": _lib.VN_ACT_GELU_TANH}
+
+
+def _elem(name: str, dtype: torch.dtype) -> int:
+    kind = _ELEM.get(dtype)
+    if kind is None:
+        raise TypeError(f"{name}: unsupported dtype {dtype} (float32 or bfloat16)")
+    return kind
+
+
+def _activation(activation: Optional[str]) -> int:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"unknown activation {activation!r}")
+    return act
+
+
+def _aligned(t: torch.Tensor) -> torch.Tensor:
+    """Dense and at a 16-byte address, as the matrix products load it."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
+    _require_device(name, t, device)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be ({n},)")
+    return t.to(torch.float32).contiguous()
+
+
+def _output(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _require_device(name, out, device)
+    if out.shape != torch.Size(shape) or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return out
+
+
+def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
+    return torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes > 0 else None
+
+
+def _linear_operands(x: torch.Tensor, weight: torch.Tensor):
+    _require_device("weight", weight)
+    _require_device("x", x, weight.device)
+    if weight.dim() != 2:
+        raise ValueError("weight must be (out_features, in_features)")
+    if x.dtype != weight.dtype:
+        raise TypeError(f"x ({x.dtype}) and weight ({weight.dtype}) must share a dtype")
+    if x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x and weight disagree on in_features")
+    return _elem("weight", weight.dtype), math.prod(x.shape[:-1])
+
+
+def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           activation: Optional[str] = None, residual: Optional[torch.Tensor] = None,
+           pre: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+           out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """``act(x @ weight^T + bias) + residual`` in one call.
+
+    x: (..., in); weight: (out, in) in x's dtype (float32 or bfloat16); bias:
+    (out,) or None; activation: None, ``"relu"``, ``"gelu"`` (erf), ``"gelu_tanh"``
+    or ``"silu"``; residual: (..., out) in the output's dtype, or None (it may be
+    ``out`` itself).  Returns (..., out) in ``out_dtype`` (x's by default).
+    ``pre``: a contiguous (..., out) tensor in x's dtype that receives
+    ``x @ weight^T + bias``, for ``linear_backward``.
+    """
+    lib = _lib.load()
+    kind, rows = _linear_operands(x, weight)
+    dev = weight.device
+    out_f, in_f = weight.shape
+    shape = x.shape[:-1] + (out_f,)
+    act = _activation(activation)
+    b = _vector("bias", bias, out_f, dev)
+    out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    out_kind = _elem("out", out_dtype)
+    y = _output("out", out, shape, out_dtype, dev)
+    if pre is not None:
+        _output("pre", pre, shape, x.dtype, dev)
+    r = None
+    if residual is not None:
+        _require_device("residual", residual, dev)
+        if residual.shape != shape or residual.dtype != out_dtype:
+            raise ValueError(f"residual must be {tuple(shape)} in {out_dtype}")
+        r = residual.contiguous()
+    xc, wc = _aligned(x), _aligned(weight)
+    need = ctypes.c_int64(0)
+    _lib.check("vn_linear_workspace_size",
+               lib.vn_linear_workspace_size(kind, rows, in_f, out_f, ctypes.byref(need)))
+    ws = _workspace(need.value, dev)
+    st = lib.vn_linear(_ptr(xc), _ptr(wc), kind, _ptr(b), _ptr(r), rows, in_f, out_f, act, out_kind, _ptr(y),
+                       _ptr(pre), _ptr(ws), need.value, _stream(dev))
+    _lib.check("vn_linear", st)
+    return y
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, activation: Optional[str] = None,
+                    pre: Optional[torch.Tensor] = None, input_gradient: bool = True, weight_gradient: bool = True,
+                    bias_gradient: bool = True, weight_gradient_dtype: Optional[torch.dtype] = None
+                    ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of ``linear``: ``(dx, dweight, dbias)``, None where not wanted.
+
+    dy: (..., out), float32 or bfloat16; x and weight as in ``linear``; ``pre``: what
+    ``linear`` stored there (needed with an activation).  dx has x's dtype,
+    dweight ``weight_gradient_dtype`` (weight's by default), dbias is float32.
+    The residual's gradient is dy itself.  With bfloat16 operands the product
+    ``dy * act'(pre)`` is rounded to bfloat16 for dx and dweight.
+    """
+    lib = _lib.load()
+    kind, rows = _linear_operands(x, weight)
+    dev = weight.device
+    out_f, in_f = weight.shape
+    shape = x.shape[:-1] + (out_f,)
+    act = _activation(activation)
+    _require_device("dy", dy, dev)
+    if dy.shape != shape:
+        raise ValueError(f"dy must be {tuple(shape)}")
+    dy_kind = _elem("dy", dy.dtype)
+    z = None
+    if act != _lib.VN_ACT_NONE:
+        if pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        _require_device("pre", pre, dev)
+        if pre.shape != shape or pre.dtype != x.dtype:
+            raise ValueError(f"pre must be {tuple(shape)} in {x.dtype}")
+        z = pre.contiguous()
+    dw_dtype = weight.dtype if weight_gradient_dtype is None else weight_gradient_dtype
+    dw_kind = _elem("weight_gradient_dtype", dw_dtype)
+    dyc, xc, wc = _aligned(dy), _aligned(x), _aligned(weight)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
+    dw = torch.empty(weight.shape, dtype=dw_dtype, device=dev) if weight_gradient else None
+    db = torch.empty((out_f,), dtype=torch.float32, device=dev) if bias_gradient else None
+    need = ctypes.c_int64(0)
+    wanted = (1 if input_gradient else 0) | (2 if weight_gradient else 0) | (4 if bias_gradient else 0)
+    _lib.check("vn_linear_backward_workspace_size",
+               lib.vn_linear_backward_workspace_size(kind, dy_kind, rows, in_f, out_f, act, wanted,
+                                                     ctypes.byref(need)))
+    ws = _workspace(need.value, dev)
+    st = lib.vn_linear_backward(_ptr(dyc), dy_kind, _ptr(xc), _ptr(wc), kind, _ptr(z), rows, in_f, out_f, act,
+                                _ptr(dx), _ptr(dw), dw_kind, _ptr(db), _ptr(ws), need.value, _stream(dev))
+    _lib.check("vn_linear_backward", st)
+    return dx, dw, db
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+               eps: float = 1e-5, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+               stats: bool = False):
+    """Layer norm over the last axis: ``(x - mean) * rstd * weight + bias``.
+
+    x: (..., n), float32 or bfloat16; weight, bias: (n,) or None.  Returns (..., n)
+    in ``out_dtype`` (x's by default), and with ``stats`` also the float32 mean and
+    1 / standard deviation of each row, (...,), for ``layer_norm_backward``.
+    """
+    lib = _lib.load()
+    _require_device("x", x)
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis to normalise")
+    n = x.shape[-1]
+    kind = _elem("x", x.dtype)
+    w, b = _vector("weight", weight, n, dev), _vector("bias", bias, n, dev)
+    out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
+    out_kind = _elem("out", out_dtype)
+    y = _output("out", out, x.shape, out_dtype, dev)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
+    xc = x.contiguous()
+    st = lib.vn_layer_norm(_ptr(xc), kind, _ptr(w), _ptr(b), math.prod(x.shape[:-1]), n, float(eps), _ptr(y),
+                           out_kind, _ptr(mean), _ptr(rstd), _stream(dev))
+    _lib.check("vn_layer_norm", st)
+    return (y, mean, rstd) if stats else y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: Optional[torch.Tensor] = None, input_gradient: bool = True,
+                        parameter_gradients: bool = True
+                        ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of ``layer_norm``: ``(dx, dweight, dbias)``, None where not wanted.
+
+    dy: (..., n), float32 or bfloat16; x, mean, rstd, weight as ``layer_norm`` took
+    and gave them.  dx has x's dtype; dweight and dbias are float32.
+    """
+    lib = _lib.load()
+    _require_device("x", x)
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x must have a last axis to normalise")
+    n = x.shape[-1]
+    rows = math.prod(x.shape[:-1])
+    kind = _elem("x", x.dtype)
+    _require_device("dy", dy, dev)
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must be {tuple(x.shape)}")
+    dy_kind = _elem("dy", dy.dtype)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _require_device(name, t, dev)
+        if t.shape != x.shape[:-1] or t.dtype != torch.float32:
+            raise ValueError(f"{name} must be {tuple(x.shape[:-1])} in float32")
+    w = _vector("weight", weight, n, dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
+    sums = torch.empty((2, n), dtype=torch.float32, device=dev) if parameter_gradients else None
+    dw, db = (sums[0], sums[1]) if parameter_gradients else (None, None)
+    need = ctypes.c_int64(0)
+    if parameter_gradients:
+        _lib.check("vn_layer_norm_backward_workspace_size",
+                   lib.vn_layer_norm_backward_workspace_size(rows, n, ctypes.byref(need)))
+    ws = _workspace(need.value, dev)
+    dyc, xc, mc, rc = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
+    st = lib.vn_layer_norm_backward(_ptr(dyc), dy_kind, _ptr(xc), kind, _ptr(w), _ptr(mc), _ptr(rc), rows, n,
+                                    _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need.value, _stream(dev))
+    _lib.check("vn_layer_norm_backward", st)
+    return dx, dw, db
+
+
+_BLOCK = 128   # state elements that share a scale; tensors start at whole blocks
+
+
+class AdamW:
+    """AdamW over many tensors, a launch for every 64 of them.
+
+    ``params``: contiguous float32 or bfloat16 tensors on one GPU, updated in place;
+    ``grads``: as many contiguous float32 or bfloat16 tensors of the same sizes,
+    read by every ``step()`` (``step(grads=...)`` takes others from then on).
+    ``weight_decay``: one number, or one for each tensor (0 for biases and norms).
+    ``copies``: contiguous bfloat16 tensors (or None entries) that receive each new
+    float32 parameter rounded, such as the weights that the layers read.
+    ``maximize``: ascend, as the evolution-strategies gradient estimators point.
+
+    ``state_bits`` 32: float32 averages.  8: fp8 codes with a power-of-two scale
+    for every 128 elements (``state["exp_avg"]`` float8_e4m3fn,
+    ``state["exp_avg_sq"]`` float8_e5m2, and their ``..._scale``: a code's value is
+    multiplied by ``2 ** (scale - 127)``; ``moments()`` gives the values).  The codes are rounded
+    by a dither that a step's number and an element's place determine, so runs
+    are reproducible.  A gradient that is not finite makes its whole block of 128 non-finite
+    from the next step on, where 32-bit states lose that element alone.
+
+    ``state``: a state to go on from, used in place: ``optimizer.state`` of another
+    AdamW over tensors of the same sizes (a dict of flat tensors, each
+    parameter's elements at ``offsets[i]``, and the number of ``"step"`` s taken).
+
+    ``device_step``: count the steps on the GPU, so that a ``step()`` captured into
+    a HIP graph counts on from replay to replay (the learning rate and the weight
+    decay stay those of the capture); ``state["step"]`` is then an int64 tensor.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], lr: float = 1e-3,
+                 betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: Union[float, Sequence[float]] = 0.01,
+                 copies: Optional[Sequence[Optional[torch.Tensor]]] = None, state_bits: int = 32,
+                 maximize: bool = False, state: Optional[Dict] = None, device_step: bool = False):
+        self._lib = _lib.load()
+        self.params = list(params)
+        n = len(self.params)
+        if n < 1:
+            raise ValueError("at least one parameter")
+        self.lr, self.betas, self.eps, self.maximize = float(lr), (float(betas[0]), float(betas[1])), float(eps), maximize
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.state_bits = state_bits
+        _require_device("params", self.params[0])
+        dev = self.device = self.params[0].device
+        self._sizes = []
+        for i, p in enumerate(self.params):
+            _require_device(f"params[{i}]", p, dev)
+            if not p.is_contiguous():
+                raise ValueError(f"params[{i}] must be contiguous: it is updated in place")
+            self._sizes.append(p.numel())
+        kinds = [_elem(f"params[{i}]", p.dtype) for i, p in enumerate(self.params)]
+        decay = [float(weight_decay)] * n if isinstance(weight_decay, (int, float)) else [float(d) for d in weight_decay]
+        if len(decay) != n:
+            raise ValueError("one weight_decay for each parameter")
+        self.copies = [None] * n if copies is None else list(copies)
+        if len(self.copies) != n:
+            raise ValueError("one copy (or None) for each parameter")
+        for i, c in enumerate(self.copies):
+            if c is None:
+                continue
+            _require_device(f"copies[{i}]", c, dev)
+            if (c.dtype != torch.bfloat16 or c.numel() != self._sizes[i] or not c.is_contiguous()
+                    or self.params[i].dtype != torch.float32):
+                raise ValueError(f"copies[{i}] must be a contiguous bfloat16 tensor of a float32 parameter's size")
+        self.offsets, total = [], 0
+        for size in self._sizes:
+            self.offsets.append(total)
+            total += -(-size // _BLOCK) * _BLOCK
+        self._total = total
+        ptrs = ctypes.c_void_p * n
+        self._numel = (ctypes.c_int64 * n)(*self._sizes)
+        self._param_kinds = (ctypes.c_int32 * n)(*kinds)
+        self._copy_ptrs = ptrs(*[0 if c is None else c.data_ptr() for c in self.copies]) if any(
+            c is not None for c in self.copies) else None
+        self._decay = (ctypes.c_double * n)(*decay)
+        self._offsets = (ctypes.c_int64 * n)(*self.offsets)
+        self._param_ptrs = ptrs(*[p.data_ptr() for p in self.params])
+        self._bound = [p.data_ptr() for p in self.params] + [c.data_ptr() for c in self.copies if c is not None]
+        self._checked = self.params + [c for c in self.copies if c is not None]
+        self._bind_grads(grads)
+        self._set_state(state, device_step)
+
+    def _bind_grads(self, grads: Sequence[torch.Tensor]):
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("one gradient for each parameter")
+        for i, g in enumerate(grads):
+            _require_device(f"grads[{i}]", g, self.device)
+            if g.numel() != self._sizes[i] or not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous and of its parameter's size")
+        n = len(grads)
+        self._grad_kinds = (ctypes.c_int32 * n)(*[_elem(f"grads[{i}]", g.dtype) for i, g in enumerate(grads)])
+        self._grad_bound = [g.data_ptr() for g in grads]
+        self._grad_ptrs = (ctypes.c_void_p * n)(*self._grad_bound)
+        self.grads = grads
+
+    def _set_state(self, state: Optional[Dict], device_step: bool):
+        dev, total = self.device, self._total
+        small = self.state_bits == 8
+        want = {"exp_avg": (torch.float8_e4m3fn if small else torch.float32, total),
+                "exp_avg_sq": (torch.float8_e5m2 if small else torch.float32, total)}
+        if small:
+            want["exp_avg_scale"] = want["exp_avg_sq_scale"] = (torch.uint8, total // _BLOCK)
+        if state is None:
+            self.state = {k: torch.zeros(n, dtype=dt, device=dev) for k, (dt, n) in want.items()}
+            start = 0
+        else:
+            self.state = {}
+            for k, (dt, n) in want.items():
+                t = state.get(k)
+                _require_device(f"state[{k!r}]", t, dev)
+                if t.dtype != dt or t.shape != (n,) or not t.is_contiguous() or t.data_ptr() % 16:
+                    raise ValueError(f"state[{k!r}] must be a contiguous, 16-byte aligned {dt} tensor of {n} elements")
+                self.state[k] = t
+            start = int(state["step"])
+            if start < 0:
+                raise ValueError("state['step'] must not be negative")
+        self.state["step"] = torch.tensor(start, dtype=torch.int64, device=dev) if device_step else start
+        self._coef = torch.empty(4, dtype=torch.float32, device=dev) if device_step else None
+
+    def step(self, grads: Optional[Sequence[torch.Tensor]] = None, lr: Optional[float] = None) -> None:
+        """One update of every parameter, in place."""
+        if grads is not None:
+            self._bind_grads(grads)
+        if lr is not None:
+            self.lr = float(lr)
+        # a tensor that was given other memory since: its old memory is not written
+        if [t.data_ptr() for t in self._checked] != self._bound or [g.data_ptr() for g in self.grads] != self._grad_bound:
+            raise ValueError("a parameter, copy or gradient has been given other memory: make a new AdamW with state=")
+        lib, s = self._lib, self.state
+        stream = _stream(self.device)
+        if self._coef is not None:
+            _lib.check("vn_adamw_coefficients",
+                       lib.vn_adamw_coefficients(_ptr(s["step"]), self.lr, *self.betas, _ptr(self._coef), stream))
+            t = 0
+        else:
+            t = s["step"] + 1
+        st = lib.vn_adamw_step(len(self.params), self._numel, self._param_ptrs, self._param_kinds, self._grad_ptrs,
+                               self._grad_kinds, self._copy_ptrs, self._decay, self._offsets, self._total,
+                               self.state_bits, _ptr(s["exp_avg"]), _ptr(s["exp_avg_sq"]),
+                               _ptr(s.get("exp_avg_scale")), _ptr(s.get("exp_avg_sq_scale")), t, self.lr,
+                               self.betas[0], self.betas[1], self.eps, 1 if self.maximize else 0, _ptr(self._coef),
+                               stream)
+        _lib.check("vn_adamw_step", st)
+        if self._coef is None:
+            s["step"] = t
+
+    def moments(self) -> List[Tuple[torch.Tensor, torch.Tensor]]:
+        """The first and second averages of each parameter, float32, in its shape."""
+        flat = []
+        for name in ("exp_avg", "exp_avg_sq"):
+            t = self.state[name]
+            if self.state_bits == 8:
+                scale = torch.exp2(self.state[name + "_scale"].to(torch.float32) - 127.0)
+                t = (t.to(torch.float32).view(-1, _BLOCK) * scale[:, None]).view(-1)
+            flat.append(t)
+        return [tuple(t[at:at + p.numel()].view(p.shape) for t in flat) for at, p in zip(self.offsets, self.params)]
