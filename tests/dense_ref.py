@@ -147,7 +147,8 @@ def adamw32(p, g, m, v, t, lr, betas, eps, wd, maximize=False):
     g = -g if maximize else g
     m = m * b1 + g * (1.0 - b1)
     v = v * b2 + (g * g) * (1.0 - b2)
-    denom = torch.sqrt(v) * (1.0 / math.sqrt(1.0 - b2 ** t)) + eps
+    # (torch's fp32 square root on the CPU is not always the nearest; through 64 bits it is)
+    denom = v.double().sqrt().float() * (1.0 / math.sqrt(1.0 - b2 ** t)) + eps
     p = p * (1.0 - lr * wd) - (m / denom) * (lr / (1.0 - b1 ** t))
     return p, m, v
 
