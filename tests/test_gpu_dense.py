@@ -611,3 +611,48 @@ def test_other_streams():
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a, b) for a, b in zip(g, want))
+
+
+# (rows, in, out) whose products have enough tiles of 256 rows: both tile widths, rows and columns off the tiles,
+# one stage of k and several, k off the stages, also in the k-major operands of the gradients
+WIDE = [(5000, 72, 2048), (6200, 200, 2056), (6144, 64, 2048), (2049, 328, 5000), (8200, 8, 1544),
+        (2049, 136, 3080), (2300, 64, 3328)]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=str)
+def test_linear_wide(shape):
+    print("linear wide", shape, flush=True)
+    m, k, n = shape
+    gen = torch.Generator().manual_seed(m + k + n)
+    x, w, b, r = (rand(gen, m, k, dtype=BF16), rand(gen, n, k, scale=k ** -0.5, dtype=BF16), rand(gen, n, scale=0.3),
+                  rand(gen, m, n, dtype=BF16))
+    pre = torch.full((m, n), float("nan"), dtype=BF16, device=device())
+    y = vn.linear(dev(x), dev(w), dev(b), activation="silu", residual=dev(r), pre=pre)
+    want, z, ez = ref.linear(x, w, b, "silu", r)
+    within(y, want, ref.linear_bound(want, z, ez, BF16, r), "y")
+    within(pre, z, ez + ref.HALF[BF16] * z.abs() * 1.01 + 1e-30, "pre")
+    assert torch.equal(vn.linear(dev(x), dev(w), dev(b), activation="silu", residual=dev(r)), y)
+    # a NaN past the end of a row's k, in the row that follows, stays in its row
+    x[m // 2, 0] = float("nan")
+    y = vn.linear(dev(x), dev(w)).cpu()
+    assert torch.isnan(y[m // 2]).all() and int(torch.isnan(y).sum()) == n
+
+
+# (rows, in, out): the input gradient on wide tiles, then the weight's
+@pytest.mark.parametrize("shape", [(5000, 2056, 72), (6200, 2048, 264), (77, 2056, 5000), (331, 2048, 6152), (64, 4096, 4096),
+                                   (2049, 3080, 72), (100, 3080, 2056)],
+                         ids=str)
+def test_linear_backward_wide(shape):
+    print("linear_backward wide", shape, flush=True)
+    m, k, n = shape
+    gen = torch.Generator().manual_seed(m + k + n)
+    x, w, dy = rand(gen, m, k, dtype=BF16), rand(gen, n, k, scale=k ** -0.5, dtype=BF16), rand(gen, m, n, dtype=BF16)
+    dx, dw, db = vn.linear_backward(dev(dy), dev(x), dev(w), weight_gradient_dtype=F32)
+    az, aw, ax = dy.double().abs(), w.double().abs(), x.double().abs()
+    want = dy.double() @ w.double()
+    within(dx, want, (n + 12) * ref.U * (az @ aw) + ref.HALF[BF16] * 1.01 * want.abs() + 1e-30, "dx")
+    want = dy.double().t() @ x.double()
+    within(dw, want, (m + 12) * ref.U * (az.t() @ ax) + ref.HALF[F32] * 1.01 * want.abs() + 1e-30, "dw")
+    within(db, dy.double().sum(0), (m + 4) * ref.U * az.sum(0) + 1e-30, "db")
+    again = vn.linear_backward(dev(dy), dev(x), dev(w), weight_gradient_dtype=F32)
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dw, db)))

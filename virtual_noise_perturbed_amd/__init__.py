@@ -45,10 +45,13 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # (the raw handle: torch.cuda.current_stream() builds a Stream object, 2 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _require_device(name: str, t: torch.Tensor, device: Optional[torch.device] = None):
+    if isinstance(t, torch.Tensor) and t.is_cuda and (device is None or t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":

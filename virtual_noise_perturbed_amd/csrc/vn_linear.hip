@@ -1,414 +1,433 @@
 // Linear layer with its epilogue, and its gradients (gfx950):
 //   z = x W^T + b,   y = act(z) + residual
 //   dz = dy act'(z), dx = dz W,  dW = dz^T x,  db = sum over rows of dz
-// Every product is one form, C[m,n] = sum_k A[m,k] B[n,k], with both operands
-// contiguous along k, on the bf16 matrix cores with fp32 accumulation:
+// Every product is one form, C[m,n] = sum_k A[m,k] B[n,k], with fp32
+// accumulation on the bf16 matrix cores:
 //   - bf16 operands as they are;
 //   - fp32 operands as three bf16 values each, v = h + m + l (h = bf16(v),
 //     m = bf16(v - h), l = bf16(v - h - m): 24 bits and more), and the six
 //     products hh, hm, mh, hl, mm, lh; what is dropped is below 2^-24 of a
 //     product.  Six bf16 products at 16x the fp32 matrix rate take 0.4 of the
 //     fp32 matrix cores' time.
-// pack_kernel brings an operand into this form where it is not: transposed
-// (W for dx; dz and x for dW), in three planes, padded along k to whole stages
-// of 64, or multiplied by act'(z).  dz is rounded to bf16 for the products of
-// bf16 operands; db is summed from the unrounded dz.
-#include <stdint.h>
+// dz is rounded to bf16 for the products of bf16 operands; db is summed from
+// the unrounded dz.
 
-#include <utility>
-
-#include "vn_dense.hpp"
-#include "vn_rows.hpp"
+#include "vn_linear.hpp"
 
 namespace vn {
 namespace {
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+// A stage: BK of k, in segments of 8 (a unit: 16 bytes of a row in bf16), in
+// PLANES bf16 planes.
+template <typename T> struct Kind;
+template <> struct Kind<float> { static constexpr int PLANES = 3, BK = 32; };
+template <> struct Kind<__bf16> { static constexpr int PLANES = 1, BK = 64; };
 
-constexpr int BK = 64;   // k per stage
-
-// ---- activations -----------------------------------------------------------
-
-__device__ __forceinline__ float act_value(Act a, float z) {
-  switch (a) {
-    case Act::relu: return z > 0.0f ? z : 0.0f;
-    case Act::gelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-    case Act::silu: return z / (1.0f + expf(-z));
-    case Act::gelu_tanh: {
-      // (1 + tanh u) / 2 = 1 / (1 + exp(-2u))
-      const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-      return z / (1.0f + expf(-2.0f * u));
-    }
-    default: return z;
-  }
+// LDS layout of a stage's operand: unit (plane, row r, segment s) is
+// plane * rows * SEGS + r * SEGS + (s ^ swz(r)); the swizzle keeps the fragment
+// reads (32 rows at one segment) free of bank conflicts.
+template <int SEGS> __device__ __forceinline__ int swz(int r) {
+  if constexpr (SEGS == 8) return (r & 7) ^ ((r >> 3) & 1);
+  else return ((r >> 1) & 3) ^ ((r >> 3) & 1);
 }
 
-__device__ __forceinline__ float act_slope(Act a, float z) {
-  switch (a) {
-    case Act::relu: return z > 0.0f ? 1.0f : 0.0f;
-    case Act::gelu:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    case Act::silu: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
-    case Act::gelu_tanh: {
-      const float u = 0.79788456080286536f * (z + 0.044715f * z * z * z);
-      const float s = 1.0f / (1.0f + expf(-2.0f * u));
-      const float du = 0.79788456080286536f * (1.0f + 3.0f * 0.044715f * z * z);
-      return s + z * s * (1.0f - s) * 2.0f * du;
-    }
-    default: return 1.0f;
-  }
-}
-
-// ---- epilogue --------------------------------------------------------------
-
-struct Epilogue {
-  const float* bias;     // by column, or null
-  const void* residual;  // in out_type, or null
-  Act act;
-  Elem out_type, pre_type;
-  void* out;             // (m, n) dense
-  void* pre;             // or null
-};
-
-__device__ __forceinline__ float load_elem(const void* p, Elem t, int64_t i) {
-  return t == Elem::f32 ? static_cast<const float*>(p)[i] : static_cast<float>(static_cast<const __bf16*>(p)[i]);
-}
-__device__ __forceinline__ void store_elem(void* p, Elem t, int64_t i, float v) {
-  if (t == Elem::f32) static_cast<float*>(p)[i] = v;
-  else static_cast<__bf16*>(p)[i] = static_cast<__bf16>(v);
-}
-
-// Output i (column's bias b) from the product's value.
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t i, float b, float acc) {
-  const float z = acc + b;
-  if (e.pre != nullptr) store_elem(e.pre, e.pre_type, i, z);
-  float y = act_value(e.act, z);
-  if (e.residual != nullptr) y += load_elem(e.residual, e.out_type, i);
-  store_elem(e.out, e.out_type, i, y);
-}
-
-// ---- the product -----------------------------------------------------------
-
-struct Product {
-  const __bf16* a;       // (m, lda), planes a_plane apart
-  const __bf16* b;       // (n, ldb), planes b_plane apart
-  int64_t a_plane, b_plane, lda, ldb;
-  int64_t m, n;
-  int32_t nk;            // stages of BK along k
-  int32_t terms;         // 1, or 6 for three planes
-  int32_t tiles_m, tiles_n, splits;
-  float* partial;        // (splits, m, n) when splits > 1
-  Epilogue e;
-};
-
-// Planes (0 h, 1 m, 2 l) of the six products of fp32 operands, smallest first;
-// two bits each.
-constexpr uint32_t kPlanesA = 2u << 0 | 1u << 2 | 0u << 4 | 1u << 6 | 0u << 8 | 0u << 10;
-constexpr uint32_t kPlanesB = 0u << 0 | 1u << 2 | 2u << 4 | 0u << 6 | 1u << 8 | 0u << 10;
-
-// LDS layout of a stage: unit (16 B) of (row r, k-segment s of 8) is
-// r*8 + (s ^ swz(r)); the swizzle keeps the fragment reads (32 rows at one
-// segment) free of bank conflicts.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
-
-// 16 bytes at each lane's address -> LDS byte address base + IMM + 16 * lane
-// (base wave-uniform).  M0 takes the LDS address; one wait state separates its
-// write from the load.  Nothing tracks the load: wait_vm before its use.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-template <int IMM>
-__device__ __forceinline__ void lds_load16(const void* p, uint32_t base) {
-  asm volatile("s_add_u32 m0, %1, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(base), "n"(IMM)
-               : "memory", "m0", "scc");
-}
-#pragma clang diagnostic pop
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
-template <typename F, int... I>
-__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void static_for(F&& f) {
-  static_for_impl(f, std::make_integer_sequence<int, N>{});
-}
-
-// Tile q of a tiles_m x tiles_n grid for workgroup `id`: consecutive ids go to
-// the 8 XCDs in turn; each XCD takes a contiguous range of an order that walks
-// groups of 4 row tiles column by column, so that its tiles share rows of A
-// and B in its L2.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
-  const uint32_t total = tiles_m * tiles_n;
-  const uint32_t x = id % 8, i = id / 8, per = total / 8, rest = total % 8;
-  const uint32_t q = x * per + (x < rest ? x : rest) + i;
-  const uint32_t first = q / (4 * tiles_n) * 4;
-  const uint32_t gsz = (tiles_m - first) < 4 ? (tiles_m - first) : 4;
-  const uint32_t r = q - first * tiles_n;
-  tm = first + r % gsz;
-  tn = r / gsz;
-}
-
-// One tile of TM x TN outputs by 4 waves (2 x 2), two LDS slots of a stage:
-// stage s + 1 is on its way while stage s is multiplied.  Rows past m or n are
-// read from the last row and not stored.
-template <int TM, int TN>
-__global__ __launch_bounds__(256, 2) void tile_kernel(Product g) {
-  constexpr int UNITS = (TM + TN) * 8, LOADS = UNITS / 256;
-  constexpr int MB = TM / 64, NB = TN / 64;   // 32-blocks per wave
-  __shared__ uint4 smem[2 * UNITS];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave & 1, wn = wave >> 1;
-  uint32_t tm, tn;
-  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
-  const int64_t m0 = static_cast<int64_t>(tm) * TM, n0 = static_cast<int64_t>(tn) * TN;
-
-  const int lrow = tid >> 3;
-  const int lseg = (tid & 7) ^ swz(lrow);
-  const uint32_t wave_lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + wave * 64 * 16;
-  const __bf16* src[LOADS];
+// 8 values as the units of their planes.
+__device__ __forceinline__ void split_planes(const float (&v)[8], uint4 (&u)[3]) {
+  uint32_t w[3][4];
 #pragma unroll
-  for (int u = 0; u < LOADS; ++u) {
-    const int row = u * 32 + lrow;
-    if (u * 32 < TM) {
-      const int64_t r = m0 + row < g.m ? m0 + row : g.m - 1;
-      src[u] = g.a + r * g.lda + lseg * 8;
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
+    // (the largest finite values would round up to infinity: their plane h is
+    // the largest bf16, and m takes the rest)
+    constexpr float kMost = 0x1.FEp127f;
+    w[0][i] = pack_bf16(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost));
+    a -= __builtin_bit_cast(float, w[0][i] << 16);
+    b -= __builtin_bit_cast(float, w[0][i] & 0xFFFF0000u);
+    w[1][i] = pack_bf16(a, b);
+    a -= __builtin_bit_cast(float, w[1][i] << 16);
+    b -= __builtin_bit_cast(float, w[1][i] & 0xFFFF0000u);
+    w[2][i] = pack_bf16(a, b);
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q) u[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+}
+
+// C consecutive elements at any element-aligned address, as they lie in memory.
+template <typename T, int C> struct Few { T e[C]; };
+template <typename T, int C> __device__ __forceinline__ Few<T, C> load_few(const T* p) {
+  typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint32_t u32_any __attribute__((aligned(2)));
+  Few<T, C> f;
+  if constexpr (sizeof(f) == 8) {
+    const u32x2_any v = *reinterpret_cast<const u32x2_any*>(p);
+    __builtin_memcpy(&f, &v, 8);
+  } else {
+    static_assert(sizeof(f) == 4);
+    const u32_any v = *reinterpret_cast<const u32_any*>(p);
+    __builtin_memcpy(&f, &v, 4);
+  }
+  return f;
+}
+
+// ROWS rows of an operand's stage on their way from memory to LDS, in the
+// registers of 256 threads: UNITS units a thread.  A row-major operand's thread
+// takes a segment of UNITS rows; a k-major one's takes UNITS neighbouring rows
+// (columns in memory) of one segment, 8 loads that it transposes in registers.
+// Rows past the end are read from the last row (k-major: from what follows in
+// memory, inside the matrix); they reach only outputs that are not stored.
+// k past the end is zero.
+template <typename T, int ROWS>
+struct Staged {
+  static constexpr int SEGS = Kind<T>::BK / 8;
+  static constexpr int UNITS = ROWS * SEGS / 256;
+  static constexpr int STRIDE = 256 / SEGS;   // threads side by side
+  union {
+    Run8<T> run[UNITS];
+    Few<T, UNITS> few[8];
+  };
+
+  // Whether the stage at k can be loaded without checks: all its k exist and,
+  // k-major, what the threads of the last row read past it lies in later k's.
+  static __device__ __forceinline__ bool whole(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
+    return k + Kind<T>::BK <= kn && (!o.k_major || r0 + ROWS <= rows || k + Kind<T>::BK + UNITS <= kn);
+  }
+
+  __device__ __forceinline__ void load(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
+    const T* p = static_cast<const T*>(o.p);
+    const int tid = threadIdx.x;
+    if (!o.k_major) {
+      const int64_t kk = k + tid % SEGS * 8;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int64_t r = r0 + u * STRIDE + tid / SEGS;
+        const T* row = p + (r < rows ? r : rows - 1) * o.ld;
+        __builtin_memcpy(&run[u], row + kk, sizeof(run[u]));
+      }
     } else {
-      const int64_t r = n0 + (row - TM) < g.n ? n0 + (row - TM) : g.n - 1;
-      src[u] = g.b + r * g.ldb + lseg * 8;
+      const int64_t kk = k + tid / STRIDE * 8;
+      const int64_t c = r0 + tid % STRIDE * UNITS;
+      const T* col = p + kk * o.ld + (c < rows ? c : rows - 1);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) few[i] = load_few<T, UNITS>(col + i * o.ld);
     }
   }
-  const int stages = g.nk * g.terms;
-  const int per = (stages + g.splits - 1) / g.splits;
-  const int begin = static_cast<int>(blockIdx.y) * per;
-  const int end = begin + per < stages ? begin + per : stages;
-  auto load_stage = [&](int s, int slot) {
-    const int term = s / g.nk;
-    const int64_t k = static_cast<int64_t>(s - term * g.nk) * BK;
-    const int64_t ka = k + ((g.terms > 1 ? (kPlanesA >> (2 * term)) & 3 : 0) * g.a_plane);
-    const int64_t kb = k + ((g.terms > 1 ? (kPlanesB >> (2 * term)) & 3 : 0) * g.b_plane);
-    const uint32_t base = __builtin_amdgcn_readfirstlane(wave_lds + slot * (UNITS * 16));
-    static_for<LOADS>([&](auto uc) {
-      constexpr int u = decltype(uc)::value;
-      lds_load16<u * 256 * 16>(src[u] + (u * 32 < TM ? ka : kb), base);
-    });
+  // The same with every element checked.
+  __device__ __forceinline__ void load_checked(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
+    const T* p = static_cast<const T*>(o.p);
+    const int tid = threadIdx.x;
+    if (!o.k_major) {
+      const int64_t kk = k + tid % SEGS * 8;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int64_t r = r0 + u * STRIDE + tid / SEGS;
+        run[u] = load_run(p + (r < rows ? r : rows - 1) * o.ld, kk, kn);
+      }
+    } else {
+      const int64_t kk = k + tid / STRIDE * 8;
+      const int64_t c = r0 + tid % STRIDE * UNITS;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < UNITS; ++j)
+          few[i].e[j] = kk + i < kn && c + j < rows ? p[(kk + i) * o.ld + c + j] : static_cast<T>(0.0f);
+    }
+  }
+
+  __device__ __forceinline__ void store_unit(uint4* lds, int r, int s, const float (&v)[8]) const {
+    uint4 u[3];
+    split_planes(v, u);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) lds[q * ROWS * SEGS + r * SEGS + (s ^ swz<SEGS>(r))] = u[q];
+  }
+  __device__ __forceinline__ void store(const Operand& o, uint4* lds) const {
+    const int tid = threadIdx.x;
+    if (!o.k_major) {
+      const int s = tid % SEGS;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int r = u * STRIDE + tid / SEGS;
+        if constexpr (sizeof(T) == 4) {
+          float v[8];
+          run_values(run[u], v);
+          store_unit(lds, r, s, v);
+        } else {
+          uint4 w;
+          __builtin_memcpy(&w, &run[u], 16);
+          lds[r * SEGS + (s ^ swz<SEGS>(r))] = w;
+        }
+      }
+    } else {
+      const int s = tid / STRIDE;
+#pragma unroll
+      for (int j = 0; j < UNITS; ++j) {
+        const int r = tid % STRIDE * UNITS + j;
+        if constexpr (sizeof(T) == 4) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = few[i].e[j];
+          store_unit(lds, r, s, v);
+        } else {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * i].e[j])) |
+                   static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * i + 1].e[j])) << 16;
+          lds[r * SEGS + (s ^ swz<SEGS>(r))] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+};
+
+// One tile of TM x TN outputs by 4 waves (2 x 2), over one split of k.  A stage
+// waits in registers while the one before it is multiplied out of LDS.  The
+// matrix cores get B's rows first, so that a lane holds 4 neighbouring columns of
+// an output row; the outputs pass through LDS once more to leave in runs of 8.
+template <typename T, int TM, int TN>
+__global__ __launch_bounds__(256, 2) void tile_kernel(Products gs) {
+  constexpr int BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES;
+  constexpr int WM = TM / 2, WN = TN / 2, MB = WM / 32, NB = WN / 32;
+  constexpr int A_UNITS = PLANES * TM * SEGS, B_UNITS = PLANES * TN * SEGS;
+  constexpr int OUT_PITCH = WN + 4;   // floats: rows of 16-byte writes spread over the banks
+  constexpr int OUT_UNITS = 4 * 32 * OUT_PITCH / 4;
+  __shared__ uint4 smem[A_UNITS + B_UNITS > OUT_UNITS ? A_UNITS + B_UNITS : OUT_UNITS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
+  const uint32_t tiles = static_cast<uint32_t>(g.tiles_m) * g.tiles_n;
+  const uint32_t id = blockIdx.x - g.first, split = id / tiles;
+  uint32_t tm, tn;
+  tile_of(id - split * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * TM, n0 = static_cast<int64_t>(tn) * TN;
+  const int64_t stages = (g.k + BK - 1) / BK;
+  const int64_t per = (stages + g.splits - 1) / g.splits;
+  const int64_t begin = split * per * BK;
+  const int64_t end = (split + 1) * per * BK < stages * BK ? (split + 1) * per * BK : stages * BK;
+
+  Staged<T, TM> sa;
+  Staged<T, TN> sb;
+  auto load = [&](int64_t k) {
+    if (Staged<T, TM>::whole(g.a, m0, g.m, k, g.k)) sa.load(g.a, m0, g.m, k, g.k);
+    else sa.load_checked(g.a, m0, g.m, k, g.k);
+    if (Staged<T, TN>::whole(g.b, n0, g.n, k, g.k)) sb.load(g.b, n0, g.n, k, g.k);
+    else sb.load_checked(g.b, n0, g.n, k, g.k);
   };
 
   const int l32 = lane & 31, lh = lane >> 5;
-  const int swl = swz(l32);
-  const int arow = (wm * (TM / 2) + l32) * 8;
-  const int brow = TM * 8 + (wn * (TN / 2) + l32) * 8;
+  const int swl = swz<SEGS>(l32);
+  const int arow = (wm * WM + l32) * SEGS;
+  const int brow = A_UNITS + (wn * WN + l32) * SEGS;
   f32x16 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[a][b] = f32x16{};
 
-  if (begin < end) load_stage(begin, 0);
-  for (int s = begin; s < end; ++s) {
-    const int slot = (s - begin) & 1;
-    wait_vm<0>();
-    __syncthreads();   // stage s is whole; the other slot's readers are done
-    if (s + 1 < end) load_stage(s + 1, slot ^ 1);
-    const uint4* st = smem + slot * UNITS;
+  if (begin < end) load(begin);
+  for (int64_t k = begin; k < end; k += BK) {
+    __syncthreads();   // the stage before is multiplied
+    sa.store(g.a, smem);
+    sb.store(g.b, smem + A_UNITS);
+    if (k + BK < end) load(k + BK);
+    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
+    for (int t = 0; t < BK / 16; ++t) {
       const int seg = (2 * t + lh) ^ swl;
-      bf16x8 fa[MB], fb[NB];
+      bf16x8 fa[PLANES][MB], fb[PLANES][NB];
 #pragma unroll
-      for (int a = 0; a < MB; ++a) fa[a] = __builtin_bit_cast(bf16x8, st[arow + a * 256 + seg]);
+      for (int q = 0; q < PLANES; ++q) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) fb[b] = __builtin_bit_cast(bf16x8, st[brow + b * 256 + seg]);
-#pragma unroll
-      for (int a = 0; a < MB; ++a)
+        for (int a = 0; a < MB; ++a)
+          fa[q][a] = __builtin_bit_cast(bf16x8, smem[q * TM * SEGS + arow + a * 32 * SEGS + seg]);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[a], fb[b], acc[a][b], 0, 0, 0);
+          fb[q][b] = __builtin_bit_cast(bf16x8, smem[q * TN * SEGS + brow + b * 32 * SEGS + seg]);
+      }
+      auto multiply = [&](int p, int q) {
+#pragma unroll
+        for (int a = 0; a < MB; ++a)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q][b], fa[p][a], acc[a][b], 0, 0, 0);
+      };
+      if constexpr (PLANES == 3) {   // smallest first
+        multiply(2, 0);
+        multiply(1, 1);
+        multiply(0, 2);
+        multiply(1, 0);
+        multiply(0, 1);
+      }
+      multiply(0, 0);
     }
   }
 
-  // Lane l holds column l % 32 of each 32-block and rows
-  // 8 * (v / 4) + 4 * (l / 32) + v % 4 for v < 16.
+  // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
+  // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS of
+  // its own; one copy of the code for all of them.
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem) + wave * 32 * OUT_PITCH;
+  constexpr int LANES = WN / 8, ROWS = 64 / LANES;   // lanes of a row, rows at a time
+  constexpr int TURNS = 32 / ROWS / 2;               // of a block, two runs a lane
+  const int64_t col = n0 + wn * WN + lane % LANES * 8;
+  const int64_t row0 = m0 + wm * WM + lane / LANES;
+  const Epilogue e = g.e;
+  float bias[8];
+  if (g.splits == 1) load_bias(e, col, g.n, bias);
+  auto epilogue = [&](auto checked_c) {
+    constexpr bool CHECKED = decltype(checked_c)::value;
+#pragma unroll 1
+    for (int p = 0; p < MB * TURNS; ++p) {
+      if (p % TURNS == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        static_for<MB>([&](auto ac) {
+          constexpr int A = decltype(ac)::value;
+          if (p == A * TURNS) {
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int64_t n = n0 + wn * (TN / 2) + b * 32 + l32;
-    if (n >= g.n) continue;
-    const float bias = g.e.bias != nullptr && g.splits == 1 ? g.e.bias[n] : 0.0f;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int a = 0; a < MB; ++a) {
-      const int64_t mb = m0 + wm * (TM / 2) + a * 32 + 4 * lh;
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(out + l32 * OUT_PITCH + b * 32 + q * 8 + lh * 4) =
+                    f32x4{acc[A][b][4 * q], acc[A][b][4 * q + 1], acc[A][b][4 * q + 2], acc[A][b][4 * q + 3]};
+            // (keeps the compiler from sinking the branches' common end, which would index the accumulators)
+            asm volatile("; block %0" ::"n"(A));
+          }
+        });
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      float z[2][8];
+      int64_t row[2];
+      bool ok[2];
+      RawRun res[2];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t m = mb + 8 * (v >> 2) + (v & 3);
-        if (m >= g.m) continue;
-        if (g.splits > 1) g.partial[(static_cast<int64_t>(blockIdx.y) * g.m + m) * g.n + n] = acc[a][b][v];
-        else finish(g.e, m * g.n + n, bias, acc[a][b][v]);
+      for (int i = 0; i < 2; ++i) {
+        row[i] = row0 + (2 * p + i) * ROWS;
+        ok[i] = row[i] < g.m && col < g.n;
+        const int r = (2 * (p % TURNS) + i) * ROWS + lane / LANES;
+        __builtin_memcpy(z[i], __builtin_assume_aligned(out + r * OUT_PITCH + lane % LANES * 8, 16), 32);
+      }
+      if (g.splits > 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (ok[i]) store_run(g.partial + (static_cast<int64_t>(split) * g.m + row[i]) * g.pitch, col, g.pitch, z[i]);
+      } else {
+        if (e.residual != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!CHECKED || ok[i]) res[i] = load_raw<CHECKED>(e.residual, e.out_type, row[i], col, g.n);
+        }
+        finish<2, CHECKED>(e, row, ok, col, g.n, bias, res, z);
       }
     }
-  }
+  };
+  if (m0 + TM <= g.m && n0 + TN <= g.n) epilogue(std::false_type{});
+  else epilogue(std::true_type{});
 }
 
-// Joins the splits' partial products in split order and finishes them.
-__global__ __launch_bounds__(256) void join_kernel(Product g) {
-  const int64_t total = g.m * g.n;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    float t = 0.0f;
-    for (int s = 0; s < g.splits; ++s) t += g.partial[s * total + i];
-    finish(g.e, i, g.e.bias != nullptr ? g.e.bias[i % g.n] : 0.0f, t);
-  }
-}
+// ---- what follows a product ------------------------------------------------
 
-// ---- packing ---------------------------------------------------------------
-
-struct Pack {
-  const void* src;       // (r, c)
-  Elem type;
-  const void* pre;       // dz = src * act'(pre), or null
-  Elem pre_type;
-  Act act;
-  int64_t r, c;
-  int32_t planes;        // 1 or 3
-  __bf16* rows;          // (r, ceil64(c)), planes rows_plane apart, or null
-  int64_t rows_plane;
-  __bf16* cols;          // (c, ceil64(r)), the transpose, or null
-  int64_t cols_plane;
-  float* sums;           // (ceil(r / 64), c): sums of 64 rows, or null
+// Joins of splits' partial products, in split order, and of the bias gradient's
+// partial sums, in row order.
+struct Joins {
+  Product g[2];
+  uint32_t blocks[2];    // of 256 runs each, 0 where there is nothing to join
+  const float* sums;     // (parts, n)
+  int64_t parts, n;
+  float* db;             // or null
 };
 
-__device__ __forceinline__ Run8<float> load_any(const void* p, Elem t, int64_t row, int64_t c, int64_t n) {
-  float v[8];
-  if (t == Elem::f32) run_values(load_run(static_cast<const float*>(p) + row * n, c, n), v);
-  else run_values(load_run(static_cast<const __bf16*>(p) + row * n, c, n), v);
-  return make_run(v, static_cast<const float*>(nullptr));
+__global__ __launch_bounds__(256) void join_kernel(Joins j) {
+  uint32_t block = blockIdx.x;
+  int which = 0;
+  if (block >= j.blocks[0]) {
+    block -= j.blocks[0];
+    which = 1;
+    if (block >= j.blocks[1]) {
+      // 64 columns by 4 waves, each a quarter of the parts
+      __shared__ float s[256];
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const int64_t c = static_cast<int64_t>(block - j.blocks[1]) * 64 + lane;
+      const int64_t per = (j.parts + 3) / 4;
+      const int64_t end = (wave + 1) * per < j.parts ? (wave + 1) * per : j.parts;
+      float t = 0.0f;
+      if (c < j.n)
+        for (int64_t k = wave * per; k < end; ++k) t += j.sums[k * j.n + c];
+      s[threadIdx.x] = t;
+      __syncthreads();
+      if (wave == 0 && c < j.n) j.db[c] = ((s[lane] + s[lane + 64]) + s[lane + 128]) + s[lane + 192];
+      return;
+    }
+  }
+  const Product& g = j.g[which];
+  const int64_t runs = g.pitch / 8;
+  const int64_t i = static_cast<int64_t>(block) * 256 + threadIdx.x;
+  if (i >= g.m * runs) return;
+  const int64_t m = i / runs, c = i % runs * 8;
+  float bias[8], z[1][8] = {};
+  RawRun res[1];
+  load_bias(g.e, c, g.n, bias);
+  if (g.e.residual != nullptr) res[0] = load_raw<true>(g.e.residual, g.e.out_type, m, c, g.n);
+  for (int s = 0; s < g.splits; ++s) {
+    float v[8];
+    run_values(load_run(g.partial + (s * g.m + m) * g.pitch, c, g.pitch), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[0][e] += v[e];
+  }
+  finish<1, true>(g.e, {m}, {true}, c, g.n, bias, res, z);
 }
 
-// The next plane of v and what it leaves: bf16(v), nearest even (towards zero
-// where that would overflow), and v minus it.
-__device__ __forceinline__ float next_plane(float& v) {
-  float h = static_cast<float>(static_cast<__bf16>(v));
-  if (fabsf(h) == __builtin_inff() && fabsf(v) < __builtin_inff())
-    h = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xFFFF0000u);
-  v -= h;
-  return h;
-}
+// dz = dy act'(pre), as the products take it, and sums of its columns over 64
+// rows each: 256 columns per workgroup, 8 a thread, 8 rows at a time.
+struct Slope {
+  const void* dy;
+  Elem dy_type;
+  const void* pre;       // or null: dz = dy
+  Elem type;             // of pre and dz
+  Act act;
+  int64_t rows, n;
+  void* dz;              // or null
+  float* sums;           // (ceil(rows / 64), n), or null
+};
 
-// 64 x 64 elements per workgroup: each thread takes 8 columns of two rows.
-// The transpose goes through LDS as dwords of a column's two rows.
-__global__ __launch_bounds__(256) void pack_kernel(Pack p) {
-  constexpr int PITCH = 33;   // dwords per column: writes of a wave hit 64 banks
-  __shared__ uint32_t tile[64 * PITCH];
-  __shared__ float colsum[4 * 64];
-  const int64_t ct = (p.c + 63) / 64, rt = (p.r + 63) / 64;
-  const int64_t cp = ct * 64, rp = rt * 64;
-  const int tid = threadIdx.x, seg = tid & 7, pair = tid >> 3;
-  for (int64_t id = blockIdx.x; id < ct * rt; id += gridDim.x) {
-    const int64_t r0 = id / ct * 64, c0 = id % ct * 64;
-    const int64_t c = c0 + seg * 8;
-    float v[2][8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t r = r0 + 2 * pair + h;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[h][i] = 0.0f;
-      if (r < p.r) {
-        run_values(load_any(p.src, p.type, r, c, p.c), v[h]);
+__global__ __launch_bounds__(256) void slope_kernel(Slope p) {
+  __shared__ float s[8 * 256];
+  const int seg = threadIdx.x & 31, group = threadIdx.x >> 5;
+  const int64_t ct = (p.n + 255) / 256;
+  const int64_t part = blockIdx.x / ct, c = (blockIdx.x % ct) * 256 + seg * 8;
+  float sum[8] = {};
+  if (c < p.n) {
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = part * 64 + i * 8 + group;
+      if (r < p.rows) {
+        float v[8];
+        raw_values(load_raw<true>(p.dy, p.dy_type, r, c, p.n), p.dy_type, v);
         if (p.pre != nullptr) {
           float z[8];
-          run_values(load_any(p.pre, p.pre_type, r, c, p.c), z);
+          raw_values(load_raw<true>(p.pre, p.type, r, c, p.n), p.type, z);
+          with_act(p.act, [&](auto act) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[h][i] *= act_slope(p.act, z[i]);
+            for (int e = 0; e < 8; ++e) v[e] *= act_slope<decltype(act)::value>(z[e]);
+          });
         }
-      }
-    }
-    if (p.sums != nullptr) {
-      // a wave holds 8 pairs of rows: over its lanes of one segment, then over the waves
-      float s[8];
+        if (p.dz != nullptr) store_values<true>(p.dz, p.type, r, c, p.n, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[i] = v[0][i] + v[1][i];
-#pragma unroll
-        for (int o = 8; o < 64; o *= 2) s[i] += __shfl_xor(s[i], o, 64);
-      }
-      if ((tid & 63) < 8) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) colsum[(tid >> 6) * 64 + seg * 8 + i] = s[i];
-      }
-      __syncthreads();
-      if (tid < 64 && c0 + tid < p.c)
-        p.sums[id / ct * p.c + c0 + tid] = ((colsum[tid] + colsum[64 + tid]) + colsum[128 + tid]) + colsum[192 + tid];
-      __syncthreads();
-    }
-    for (int q = 0; q < p.planes; ++q) {
-      uint32_t w[2][4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = next_plane(v[h][2 * i]), b = next_plane(v[h][2 * i + 1]);
-          w[h][i] = pack_bf16(a, b);
-        }
-      if (p.rows != nullptr) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t r = r0 + 2 * pair + h;
-          if (r < p.r) *reinterpret_cast<uint4*>(p.rows + q * p.rows_plane + r * cp + c) = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
-        }
-      }
-      if (p.cols != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tile[(seg * 8 + 2 * i) * PITCH + pair] = (w[0][i] & 0xFFFFu) | (w[1][i] << 16);
-          tile[(seg * 8 + 2 * i + 1) * PITCH + pair] = (w[0][i] >> 16) | (w[1][i] & 0xFFFF0000u);
-        }
-        __syncthreads();
-        const int col = tid >> 2, part = tid & 3;   // 16 rows of a column
-        if (c0 + col < p.c) {
-          uint32_t t[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) t[i] = tile[col * PITCH + part * 8 + i];
-          uint4* d = reinterpret_cast<uint4*>(p.cols + q * p.cols_plane + (c0 + col) * rp + r0 + part * 16);
-          d[0] = make_uint4(t[0], t[1], t[2], t[3]);
-          d[1] = make_uint4(t[4], t[5], t[6], t[7]);
-        }
-        __syncthreads();
+        for (int e = 0; e < 8; ++e) sum[e] += v[e];
       }
     }
   }
+  if (p.sums == nullptr) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[group * 256 + seg * 8 + e] = sum[e];
+  __syncthreads();
+  const int64_t out = (blockIdx.x % ct) * 256 + threadIdx.x;
+  float t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) t += s[k * 256 + threadIdx.x];
+  if (out < p.n) p.sums[part * p.n + out] = t;
 }
 
 // ---- plans -----------------------------------------------------------------
-
-int64_t ceil64(int64_t v) { return (v + 63) / 64 * 64; }
-
-struct Plan {
-  int tile;       // 128 or 64
-  int splits;
-};
-
-Plan plan_product(int64_t m, int64_t n, int64_t stages) {   // m, n > 0
-  const int64_t t128 = ((m + 127) / 128) * ((n + 127) / 128);
-  Plan p;
-  p.tile = t128 >= 256 ? 128 : 64;
-  const int64_t tiles = ((m + p.tile - 1) / p.tile) * ((n + p.tile - 1) / p.tile);
-  int64_t s = 512 / tiles;
-  if (s > stages / 4) s = stages / 4;
-  p.splits = static_cast<int>(s < 1 ? 1 : s);
-  return p;
-}
-
-int64_t partial_bytes(int64_t m, int64_t n, int64_t stages) {
-  if (m == 0 || n == 0) return 0;
-  const Plan p = plan_product(m, n, stages);
-  return p.splits > 1 ? p.splits * m * n * 4 : 0;
-}
 
 // Takes pieces of the workspace, 256-byte aligned; with a null base it only counts.
 struct Arena {
@@ -422,143 +441,165 @@ struct Arena {
   }
 };
 
-hipError_t run_pack(const Pack& p, hipStream_t stream) {
-  const int64_t tiles = ((p.c + 63) / 64) * ((p.r + 63) / 64);
-  if (tiles == 0) return hipSuccess;
-  pack_kernel<<<static_cast<unsigned>(tiles < (1 << 20) ? tiles : (1 << 20)), 256, 0, stream>>>(p);
-  return hipGetLastError();
+int64_t tiles_of(const Product& g, int tile) {
+  return ((g.m + tile - 1) / tile) * ((g.n + tile - 1) / tile);
 }
 
-hipError_t run_product(Product g, hipStream_t stream) {
-  if (g.m == 0 || g.n == 0) return hipSuccess;
-  const Plan p = plan_product(g.m, g.n, static_cast<int64_t>(g.nk) * g.terms);
-  g.splits = p.splits;
-  g.tiles_m = static_cast<int32_t>((g.m + p.tile - 1) / p.tile);
-  g.tiles_n = static_cast<int32_t>((g.n + p.tile - 1) / p.tile);
-  const dim3 grid(static_cast<unsigned>(static_cast<int64_t>(g.tiles_m) * g.tiles_n), static_cast<unsigned>(p.splits));
-  if (p.tile == 128) tile_kernel<128, 128><<<grid, 256, 0, stream>>>(g);
-  else tile_kernel<64, 64><<<grid, 256, 0, stream>>>(g);
-  if (p.splits > 1) {
-    const int64_t blocks = (g.m * g.n + 255) / 256;
-    join_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, stream>>>(g);
+// The tile's side and the splits of the products of one launch.
+int plan(Products& gs, Elem type, Arena& ws) {
+  const int bk = type == Elem::f32 ? 32 : 64;
+  int64_t work[2] = {0, 0};   // stages of all tiles of 64, of 128
+  for (int i = 0; i < gs.count; ++i)
+    for (int t = 0; t < 2; ++t) work[t] += tiles_of(gs.g[i], 64 << t) * ((gs.g[i].k + bk - 1) / bk);
+  // Tiles of 128 where every one of the 512 that the card holds gets 16 stages:
+  // 2048^3 in fp32 takes 115 us on them, 140 on tiles of 64; 777 x 1024 x 1000's
+  // gradients 50 and 47.
+  const int tile = work[1] >= 512 * 16 ? 128 : 64;
+  const int64_t total = work[tile / 128], slots = tile == 128 ? 512 : 1024;
+  // A workgroup's stages: an equal share of all, but enough to repay a split's
+  // partial sums and their join (1000^3 in bf16: 16 us whole, 22 us in splits of 4).
+  const int64_t least = type == Elem::f32 ? 5 : 8;
+  const int64_t share = total / slots < least ? least : total / slots;
+  uint32_t first = 0;
+  for (int i = 0; i < gs.count; ++i) {
+    Product& g = gs.g[i];
+    const int64_t stages = (g.k + bk - 1) / bk;
+    const int64_t s = stages / share;
+    g.splits = static_cast<int>(s < 1 ? 1 : s);
+    g.tiles_m = static_cast<int32_t>((g.m + tile - 1) / tile);
+    g.tiles_n = static_cast<int32_t>((g.n + tile - 1) / tile);
+    g.first = first;
+    first += static_cast<uint32_t>(tiles_of(g, tile) * g.splits);
+    g.pitch = (g.n + 7) / 8 * 8;
+    g.partial = g.splits > 1 ? ws.take<float>(g.splits * g.m * g.pitch * 4) : nullptr;
   }
-  return hipGetLastError();
+  return tile;
 }
 
-// An operand of a product: where it lies, or the packing that makes it.
-struct Operand {
-  const __bf16* p;
-  int64_t ld, plane;
-};
+template <typename T>
+void launch_tiles(const Products& gs, int tile, unsigned blocks, hipStream_t stream) {
+  if (tile == 128) tile_kernel<T, 128, 128><<<blocks, 256, 0, stream>>>(gs);
+  else tile_kernel<T, 64, 64><<<blocks, 256, 0, stream>>>(gs);
+}
 
-int planes_of(Elem t) { return t == Elem::f32 ? 3 : 1; }
-int terms_of(Elem t) { return t == Elem::f32 ? 6 : 1; }
-bool direct(Elem t, int64_t k) { return t == Elem::bf16 && k % 64 == 0; }
+// The width of the wide tiles for a product, or 0: the tiles of `plan`.  What a
+// stage of k costs all tiles, in us, measured on 4096 x k x 4096 and 2048^3 (bf16):
+// 1.38 a round of 256 tiles of 256 x 256, 0.8 a round of 256 x 128, and 0.0065 for
+// each 256 x 128 of the output on plan's tiles, which fill the card at any count.
+int wide_width(const Product& g, Elem type) {
+  if (type != Elem::bf16 || !wide_applies(g)) return 0;
+  const int64_t t256 = ((g.m + 255) / 256) * ((g.n + 255) / 256), t128 = ((g.m + 255) / 256) * ((g.n + 127) / 128);
+  const double c256 = 1.38 * static_cast<double>((t256 + 255) / 256);
+  const double c128 = 0.8 * static_cast<double>((t128 + 255) / 256);
+  const double narrow = 0.0065 * static_cast<double>(t128);
+  if (narrow < c256 && narrow < c128) return 0;
+  return c256 <= c128 ? 256 : 128;
+}
 
-// The row-major operand (r, c) of a product over c.
-Operand rows_operand(const void* src, Elem t, int64_t r, int64_t c, Arena& ws, hipStream_t stream, hipError_t& err) {
-  if (direct(t, c)) return {static_cast<const __bf16*>(src), c, 0};
-  const int64_t ld = ceil64(c), plane = r * ld;
-  __bf16* d = ws.take<__bf16>(planes_of(t) * plane * 2);
-  if (ws.base != nullptr && err == hipSuccess) {
-    Pack p{};
-    p.src = src;
-    p.type = t;
-    p.r = r;
-    p.c = c;
-    p.planes = planes_of(t);
-    p.rows = d;
-    p.rows_plane = plane;
-    err = run_pack(p, stream);
+// Launches the products that take wide tiles; keeps the others.
+hipError_t run_wide(Products& gs, Elem type, bool run, hipStream_t stream) {
+  int kept = 0;
+  for (int i = 0; i < gs.count; ++i) {
+    const int w = wide_width(gs.g[i], type);
+    if (w == 0) {
+      gs.g[kept++] = gs.g[i];
+    } else if (run) {
+      const hipError_t err = launch_wide(gs.g[i], w, stream);
+      if (err != hipSuccess) return err;
+    }
   }
-  return {d, ld, plane};
+  gs.count = kept;
+  return hipSuccess;
 }
 
-// The transpose of (r, c) as an operand of a product over r.
-Operand cols_operand(const void* src, Elem t, int64_t r, int64_t c, Arena& ws, hipStream_t stream, hipError_t& err) {
-  const int64_t ld = ceil64(r), plane = c * ld;
-  __bf16* d = ws.take<__bf16>(planes_of(t) * plane * 2);
-  if (ws.base != nullptr && err == hipSuccess) {
-    Pack p{};
-    p.src = src;
-    p.type = t;
-    p.r = r;
-    p.c = c;
-    p.planes = planes_of(t);
-    p.cols = d;
-    p.cols_plane = plane;
-    err = run_pack(p, stream);
+// The products, the joins of their splits and of a bias gradient's sums.
+hipError_t run_products(const Products& gs, int tile, Elem type, Joins j, hipStream_t stream) {
+  if (gs.count > 0) {
+    const Product& last = gs.g[gs.count - 1];
+    const unsigned blocks = last.first + static_cast<unsigned>(tiles_of(last, tile) * last.splits);
+    if (type == Elem::f32) launch_tiles<float>(gs, tile, blocks, stream);
+    else launch_tiles<__bf16>(gs, tile, blocks, stream);
   }
-  return {d, ld, plane};
-}
-
-Product product_of(const Operand& a, const Operand& b, Elem t, int64_t m, int64_t n, int64_t k, Arena& ws) {
-  Product g{};
-  g.a = a.p;
-  g.b = b.p;
-  g.a_plane = a.plane;
-  g.b_plane = b.plane;
-  g.lda = a.ld;
-  g.ldb = b.ld;
-  g.m = m;
-  g.n = n;
-  g.nk = static_cast<int32_t>((k + 63) / 64);
-  g.terms = terms_of(t);
-  g.partial = ws.take<float>(partial_bytes(m, n, static_cast<int64_t>(g.nk) * g.terms));
-  return g;
+  unsigned blocks = 0;
+  for (int i = 0; i < 2; ++i) {
+    j.blocks[i] = 0;
+    if (i >= gs.count || gs.g[i].splits == 1) continue;
+    j.g[i] = gs.g[i];
+    j.blocks[i] = static_cast<uint32_t>((gs.g[i].m * (gs.g[i].pitch / 8) + 255) / 256);
+    blocks += j.blocks[i];
+  }
+  if (j.db != nullptr) blocks += static_cast<unsigned>((j.n + 63) / 64);
+  if (blocks > 0) join_kernel<<<blocks, 256, 0, stream>>>(j);
+  return gs.count > 0 || blocks > 0 ? hipGetLastError() : hipSuccess;
 }
 
 // The forward's steps; with a null workspace they only count its bytes.
 hipError_t linear_steps(const LinearParams& p, Arena& ws, hipStream_t stream) {
-  hipError_t err = hipSuccess;
-  const Operand a = rows_operand(p.x, p.type, p.rows, p.in, ws, stream, err);
-  const Operand b = rows_operand(p.w, p.type, p.out, p.in, ws, stream, err);
-  Product g = product_of(a, b, p.type, p.rows, p.out, p.in, ws);
+  Products gs{};
+  gs.count = 1;
+  Product& g = gs.g[0];
+  g.a = {p.x, p.in, false};
+  g.b = {p.w, p.in, false};
+  g.m = p.rows;
+  g.n = p.out;
+  g.k = p.in;
   g.e = {p.bias, p.residual, p.act, p.out_type, p.type, p.y, p.pre};
-  if (ws.base == nullptr || err != hipSuccess) return err;
-  return run_product(g, stream);
+  const hipError_t err = run_wide(gs, p.type, ws.base != nullptr, stream);
+  if (err != hipSuccess) return err;
+  const int tile = plan(gs, p.type, ws);
+  if (ws.base == nullptr) return hipSuccess;
+  return run_products(gs, tile, p.type, Joins{}, stream);
 }
 
 hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need_dw, bool need_db, Arena& ws,
                           hipStream_t stream) {
-  hipError_t err = hipSuccess;
   const bool run = ws.base != nullptr;
-  const int planes = planes_of(p.type);
-  // dz: its rows for dx (dy itself where that serves), its columns for dW, its sums for db
-  const bool plain = p.act == Act::none && p.dy_type == p.type && direct(p.type, p.out);
-  const int64_t ld_rows = ceil64(p.out), ld_cols = ceil64(p.rows), parts = (p.rows + 63) / 64;
-  Pack z{};
-  z.src = p.dy;
-  z.type = p.dy_type;
-  z.pre = p.act == Act::none ? nullptr : p.pre;
-  z.pre_type = p.type;
-  z.act = p.act;
-  z.r = p.rows;
-  z.c = p.out;
-  z.planes = planes;
-  z.rows_plane = p.rows * ld_rows;
-  z.cols_plane = p.out * ld_cols;
-  if (need_dx && !plain) z.rows = ws.take<__bf16>(planes * z.rows_plane * 2);
-  if (need_dw) z.cols = ws.take<__bf16>(planes * z.cols_plane * 2);
+  const int64_t size = p.type == Elem::f32 ? 4 : 2;
+  need_dx = need_dx && p.rows > 0 && p.in > 0;
+  need_dw = need_dw && p.out > 0 && p.in > 0;
+  need_db = need_db && p.out > 0;
+  // dz is dy itself where that serves
+  const bool plain = p.act == Act::none && p.dy_type == p.type;
+  const bool need_dz = !plain && (need_dx || need_dw) && p.rows > 0 && p.out > 0;
+  const int64_t parts = (p.rows + 63) / 64;
+  Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr};
+  if (need_dz) z.dz = ws.take<char>(p.rows * p.out * size);
   if (need_db) z.sums = ws.take<float>(parts * p.out * 4);
-  if (run && (z.rows != nullptr || z.cols != nullptr || z.sums != nullptr)) err = run_pack(z, stream);
-  if (run && need_db && err == hipSuccess && p.out > 0)
-    err = launch_join_columns(z.sums, parts, p.out, p.out, p.db, nullptr, stream);
+  Products gs{};
+  const void* dz = need_dz ? z.dz : p.dy;
   if (need_dx) {
-    const Operand a = plain ? Operand{static_cast<const __bf16*>(p.dy), p.out, 0} : Operand{z.rows, ld_rows, z.rows_plane};
-    const Operand b = cols_operand(p.w, p.type, p.out, p.in, ws, stream, err);
-    Product g = product_of(a, b, p.type, p.rows, p.in, p.out, ws);
+    Product& g = gs.g[gs.count++];
+    g.a = {dz, p.out, false};
+    g.b = {p.w, p.in, true};
+    g.m = p.rows;
+    g.n = p.in;
+    g.k = p.out;
     g.e = {nullptr, nullptr, Act::none, p.type, p.type, p.dx, nullptr};
-    if (run && err == hipSuccess) err = run_product(g, stream);
   }
   if (need_dw) {
-    const Operand a{z.cols, ld_cols, z.cols_plane};
-    const Operand b = cols_operand(p.x, p.type, p.rows, p.in, ws, stream, err);
-    Product g = product_of(a, b, p.type, p.out, p.in, p.rows, ws);
+    Product& g = gs.g[gs.count++];
+    g.a = {dz, p.out, true};
+    g.b = {p.x, p.in, true};
+    g.m = p.out;
+    g.n = p.in;
+    g.k = p.rows;
     g.e = {nullptr, nullptr, Act::none, p.dw_type, p.type, p.dw, nullptr};
-    if (run && err == hipSuccess) err = run_product(g, stream);
   }
-  return err;
+  if (run && (need_dz || need_db) && parts > 0) {
+    slope_kernel<<<static_cast<unsigned>(parts * ((p.out + 255) / 256)), 256, 0, stream>>>(z);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  const hipError_t err = run_wide(gs, p.type, run, stream);
+  if (err != hipSuccess) return err;
+  const int tile = plan(gs, p.type, ws);
+  if (!run) return hipSuccess;
+  Joins j{};
+  j.sums = z.sums;
+  j.parts = parts;
+  j.n = p.out;
+  j.db = need_db ? p.db : nullptr;
+  return run_products(gs, tile, p.type, j, stream);
 }
 
 }  // namespace

@@ -1,0 +1,252 @@
+// What the linear layer's kernels share (vn_linear.hip, vn_linear_wide.hip):
+// activations, the epilogue, the form of a product.
+#pragma once
+
+#include <stdint.h>
+
+#include <utility>
+
+#include "vn_dense.hpp"
+#include "vn_rows.hpp"
+
+namespace vn {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// f(std::integral_constant<int, I>) for I = 0 .. N-1, unrolled at compile time.
+template <typename F, int... I>
+__device__ __forceinline__ void static_for_impl(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
+// ---- activations -----------------------------------------------------------
+// The hardware's exponential and reciprocal (a unit of the last place each); the
+// rounding of x log2(e) is put right, so that large arguments keep that accuracy.
+
+__device__ __forceinline__ float exp_of(float x) {
+  x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);   // 0 and infinity past fp32's range
+  const float t = x * 1.44269504088896341f;
+  const float rest = __builtin_fmaf(x, 1.44269504088896341f, -t) + x * 1.92596299e-8f;
+  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.69314718055994531f, 1.0f);
+}
+__device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
+
+// The normal distribution's integral up to z, within 1.0e-7, and e = exp(-z^2 / 2):
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, whose
+// factor exp(-x^2) at x = |z| / sqrt(2) is e.  Half of erff's instructions, and the
+// lower tail is no difference to 1.
+__device__ __forceinline__ float normal_of(float z, float& e) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+  float p = __builtin_fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  p = __builtin_fmaf(t, p, 0.5f * 1.421413741f);
+  p = __builtin_fmaf(t, p, 0.5f * -0.284496736f);
+  p = __builtin_fmaf(t, p, 0.5f * 0.254829592f);
+  e = exp_of(-0.5f * z * z);
+  const float tail = t * p * e;
+  return z > 0.0f ? 1.0f - tail : tail;
+}
+
+constexpr float kTanhScale = 2.0f * 0.79788456080286536f;   // (1 + tanh u) / 2 = sigmoid(2u)
+
+template <Act A>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (A == Act::relu) {
+    return z > 0.0f ? z : 0.0f;
+  } else if constexpr (A == Act::gelu) {
+    float e;
+    return z * normal_of(z, e);
+  } else if constexpr (A == Act::silu) {
+    return z * sigmoid_of(z);
+  } else if constexpr (A == Act::gelu_tanh) {
+    return z * sigmoid_of(kTanhScale * (z + 0.044715f * z * z * z));
+  } else {
+    return z;
+  }
+}
+
+template <Act A>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (A == Act::relu) {
+    return z > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (A == Act::gelu) {
+    float e;
+    const float p = normal_of(z, e);
+    return p + z * e * 0.39894228040143268f;
+  } else if constexpr (A == Act::silu) {
+    const float s = sigmoid_of(z);
+    return s * (1.0f + z * (1.0f - s));
+  } else if constexpr (A == Act::gelu_tanh) {
+    const float s = sigmoid_of(kTanhScale * (z + 0.044715f * z * z * z));
+    return s + z * s * (1.0f - s) * (kTanhScale * (1.0f + 3.0f * 0.044715f * z * z));
+  } else {
+    return 1.0f;
+  }
+}
+
+// f(std::integral_constant<Act, a>): the choice once for many values, which then
+// go through the activation side by side.
+template <typename F>
+__device__ __forceinline__ void with_act(Act a, F&& f) {
+  switch (a) {
+    case Act::relu: f(std::integral_constant<Act, Act::relu>{}); break;
+    case Act::gelu: f(std::integral_constant<Act, Act::gelu>{}); break;
+    case Act::silu: f(std::integral_constant<Act, Act::silu>{}); break;
+    case Act::gelu_tanh: f(std::integral_constant<Act, Act::gelu_tanh>{}); break;
+    default: break;
+  }
+}
+
+// ---- epilogue --------------------------------------------------------------
+
+struct Epilogue {
+  const float* bias;     // by column, or null
+  const void* residual;  // in out_type, or null
+  Act act;
+  Elem out_type, pre_type;
+  void* out;             // (m, n) dense
+  void* pre;             // or null
+};
+
+// 8 elements of either type as they lie in memory.
+struct RawRun {
+  u32x4_any a, b;        // b: fp32 alone
+};
+
+// Elements (row, c .. c + 7) of a dense (., n); CHECKED: cut at n.
+template <bool CHECKED>
+__device__ __forceinline__ RawRun load_raw(const void* p, Elem t, int64_t row, int64_t c, int64_t n) {
+  RawRun r;
+  if (t == Elem::f32) {
+    const float* q = static_cast<const float*>(p) + row * n;
+    Run8<float> f;
+    if constexpr (CHECKED) f = load_run(q, c, n);
+    else __builtin_memcpy(&f, q + c, 32);
+    r.a = f.a;
+    r.b = f.b;
+  } else {
+    const __bf16* q = static_cast<const __bf16*>(p) + row * n;
+    Run8<__bf16> f;
+    if constexpr (CHECKED) f = load_run(q, c, n);
+    else __builtin_memcpy(&f, q + c, 16);
+    r.a = f.a;
+  }
+  return r;
+}
+__device__ __forceinline__ void raw_values(const RawRun& r, Elem t, float (&v)[8]) {
+  if (t == Elem::f32) run_values(Run8<float>{r.a, r.b}, v);
+  else run_values(Run8<__bf16>{r.a}, v);
+}
+template <bool CHECKED>
+__device__ __forceinline__ void store_values(void* p, Elem t, int64_t row, int64_t c, int64_t n, const float (&v)[8]) {
+  if (t == Elem::f32) {
+    float* q = static_cast<float*>(p) + row * n;
+    if constexpr (CHECKED) {
+      store_run(q, c, n, v);
+    } else {
+      const Run8<float> r = make_run(v, q);
+      __builtin_memcpy(q + c, &r, 32);
+    }
+  } else {
+    __bf16* q = static_cast<__bf16*>(p) + row * n;
+    if constexpr (CHECKED) {
+      store_run(q, c, n, v);
+    } else {
+      const Run8<__bf16> r = make_run(v, q);
+      __builtin_memcpy(q + c, &r, 16);
+    }
+  }
+}
+
+// The bias of columns c .. c + 7 (zeros without one).
+__device__ __forceinline__ void load_bias(const Epilogue& e, int64_t c, int64_t n, float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+  if (e.bias != nullptr && c < n) run_values(load_run(e.bias, c, n), b);
+}
+
+// Outputs (row[i], c .. c + 7) for i < R where ok[i], from the products' values z.
+// `res` holds the residual's runs where there is one.
+template <int R, bool CHECKED>
+__device__ __forceinline__ void finish(const Epilogue& e, const int64_t (&row)[R], const bool (&ok)[R], int64_t c,
+                                       int64_t n, const float (&bias)[8], const RawRun (&res)[R], float (&z)[R][8]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[i][j] += bias[j];
+  if (e.pre != nullptr) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (!CHECKED || ok[i]) store_values<CHECKED>(e.pre, e.pre_type, row[i], c, n, z[i]);
+  }
+  with_act(e.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] = act_value<decltype(act)::value>(z[i][j]);
+  });
+  if (e.residual != nullptr) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float r[8];
+      raw_values(res[i], e.out_type, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[i][j] += r[j];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (!CHECKED || ok[i]) store_values<CHECKED>(e.out, e.out_type, row[i], c, n, z[i]);
+}
+
+// ---- products --------------------------------------------------------------
+
+// A matrix as an operand: element (r, k) at r * ld + k, or where k_major at
+// k * ld + r.
+struct Operand {
+  const void* p;
+  int64_t ld;
+  bool k_major;
+};
+
+struct Product {
+  Operand a, b;          // of one type
+  int64_t m, n, k;
+  int32_t tiles_m, tiles_n, splits;
+  uint32_t first;        // its first workgroup in the launch
+  float* partial;        // (splits, m, pitch) when splits > 1
+  int64_t pitch;         // n rounded up to 8
+  Epilogue e;
+};
+
+struct Products {
+  Product g[2];
+  int32_t count;
+};
+
+// Tile q of a tiles_m x tiles_n grid for workgroup `id`: consecutive ids go to
+// the 8 XCDs in turn; each XCD takes a contiguous range of an order that walks
+// groups of 4 row tiles column by column, so that its tiles share rows of A
+// and B in its L2.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm, uint32_t& tn) {
+  const uint32_t total = tiles_m * tiles_n;
+  const uint32_t x = id % 8, i = id / 8, per = total / 8, rest = total % 8;
+  const uint32_t q = x * per + (x < rest ? x : rest) + i;
+  const uint32_t first = q / (4 * tiles_n) * 4;
+  const uint32_t gsz = (tiles_m - first) < 4 ? (tiles_m - first) : 4;
+  const uint32_t r = q - first * tiles_n;
+  tm = first + r % gsz;
+  tn = r / gsz;
+}
+
+// The product's launch on tiles of 256 rows (vn_linear_wide.hip), for bf16
+// operands that wide_applies to; tiles of 256 x tn (256 or 128), no splits.
+bool wide_applies(const Product& g);
+hipError_t launch_wide(Product g, int tn, hipStream_t stream);
+
+}  // namespace vn

@@ -1,0 +1,350 @@
+// The linear layer's large bf16 products (gfx950): C[m,n] = sum_k A[m,k] B[n,k]
+// on tiles of 256 x TN, operands row-major or k-major, straight from memory to
+// LDS and through the transposing LDS reads to the matrix cores, so that no
+// product needs a transposed copy of an operand.
+//
+// One workgroup of 4 waves per CU; each wave owns a 128 x TN/2 quarter of the
+// tile in accumulator registers.  k advances in stages of 64 through two LDS
+// slots, filled by direct global->LDS loads.  Fragments of the next k-step of 16
+// and the loads of coming stages are issued between the MFMAs, one at a time, so
+// that neither the LDS nor the address unit sees a burst.  The loads are issued
+// through inline asm and every wait on them is explicit (vmcnt before the
+// barrier that publishes a stage).
+#include "vn_linear.hpp"
+
+namespace vn {
+namespace {
+
+constexpr int BK = 64, TM = 256;
+
+// 16 bytes at sbase + voff (a wave-uniform 64-bit base, a 32-bit per-lane
+// offset) -> LDS byte address base + IMM + 16 * lane (base wave-uniform).
+// M0 takes the LDS address; one wait state separates its write from the load.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+template <int IMM>
+__device__ __forceinline__ void lds_load16(uint32_t voff, const void* sbase, uint32_t base) {
+  asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "s"(base), "n"(IMM)
+               : "memory", "m0", "scc");
+}
+#pragma clang diagnostic pop
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// LDS layout of ROWS rows of an operand's stage, in units of 16 bytes:
+//   row-major: unit (row r, segment s of 8 k) at r * 8 + (s ^ swz(r)): the
+//     fragment reads, 32 rows at one segment, are free of bank conflicts;
+//   k-major: unit (k, segment s of 8 rows) at k * ROWS / 8 + (s ^ 4 (k & 3)): a
+//     transposing read takes 4 k of 32 rows, 64 bytes each, from all 64 banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+// Loads and fragment reads of one operand: ROWS rows of the tile from row r0 on.
+template <int ROWS, bool K_MAJOR>
+struct Side {
+  static constexpr int LOADS = ROWS / 32;    // 16-byte loads a thread and stage
+  static constexpr int SEGS = ROWS / 8;      // k-major: units of a k
+  static constexpr int K_PER = 256 / SEGS;   // k-major: k of one load of the workgroup
+  const char* base;      // of the tile at k = 0
+  int64_t step;          // bytes per k
+  uint32_t pitch;        // bytes per row (k-major: per k)
+  uint32_t voff[LOADS];  // this lane's bytes from base + k * step
+
+  __device__ __forceinline__ void init(const Operand& o, int64_t r0, int64_t rows) {
+    const int tid = threadIdx.x;
+    pitch = static_cast<uint32_t>(o.ld * 2);
+    if constexpr (!K_MAJOR) {
+      base = static_cast<const char*>(o.p) + r0 * o.ld * 2;
+      step = 2;
+      const int row = tid >> 3;
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {
+        const int64_t r = r0 + u * 32 + row < rows ? u * 32 + row : rows - 1 - r0;
+        voff[u] = static_cast<uint32_t>(r) * pitch + ((tid & 7) ^ swz(row)) * 16;
+      }
+    } else {
+      base = static_cast<const char*>(o.p) + r0 * 2;
+      step = o.ld * 2;
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u) {
+        const int k = u * K_PER + tid / SEGS;
+        const int64_t c = r0 + ((tid % SEGS) ^ (4 * (k & 3))) * 8;
+        voff[u] = static_cast<uint32_t>(k) * pitch + static_cast<uint32_t>((c < rows ? c : rows - 8) - r0) * 2;
+      }
+    }
+  }
+  // Load u of the stage at k into the slot at `lds` (the byte address of this
+  // wave's first unit); `left` is how many k exist from there on.
+  template <int U, bool CHECKED>
+  __device__ __forceinline__ void load(uint32_t lds, int64_t k, int64_t left) const {
+    uint32_t v = voff[U];
+    if (CHECKED && left < BK) {   // the last, ragged stage: k past the end from the first or the last k, zeroed later
+      if constexpr (!K_MAJOR) {
+        const uint32_t seg = (threadIdx.x & 7) ^ swz(threadIdx.x >> 3);
+        if (seg * 8 >= left) v -= seg * 16;
+      } else {
+        const uint32_t kk = U * K_PER + threadIdx.x / SEGS;
+        if (kk >= left) v -= (kk - static_cast<uint32_t>(left - 1)) * pitch;
+      }
+    }
+    lds_load16<U * 256 * 16>(v, base + k * step, lds);
+  }
+  // Zeros for the k past the end of the ragged stage in `slot`.
+  static __device__ __forceinline__ void zero(uint4* slot, int64_t left) {
+    for (int u = threadIdx.x; u < ROWS * 8; u += 256) {
+      const int k = K_MAJOR ? u / SEGS : ((u & 7) ^ swz(u >> 3)) * 8;
+      if (k >= left) slot[u] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  // The fragment of 32 rows from row `row` on, k-step t: lane l holds row
+  // l % 32 and k = 8 (l / 32) .. + 7 of the step.
+  static __device__ __forceinline__ bf16x8 fragment(const uint4* slot, int row, int t, int lane) {
+    if constexpr (!K_MAJOR) {
+      const int r = row + (lane & 31);
+      return __builtin_bit_cast(bf16x8, slot[r * 8 + ((2 * t + (lane >> 5)) ^ swz(lane & 31))]);
+    } else {
+      // In each 16 lanes, lane i supplies 4 rows from 4 (i % 4) on at k = i / 4
+      // and receives row i at 4 k.
+      typedef short s16x4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) s16x4* LdsPtr;
+      const int i = lane & 15;
+      const int s = row / 8 + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+      const int k = 16 * t + 8 * (lane >> 5) + (i >> 2);   // k & 3 = i / 4
+      const char* p = reinterpret_cast<const char*>(slot + k * SEGS + (s ^ (4 * (i >> 2)))) + (i & 1) * 8;
+      struct { s16x4 a, b; } f;
+      f.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)p);
+      f.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsPtr)(p + 4 * SEGS * 16));
+      return __builtin_bit_cast(bf16x8, f);
+    }
+  }
+};
+
+template <int TN, bool A_K, bool B_K>
+__global__ __launch_bounds__(256, 1) void wide_kernel(Product g) {
+  constexpr int NB = TN / 64;                     // 32-blocks of a wave's columns
+  constexpr int A_UNITS = TM * 8, UNITS = A_UNITS + TN * 8;
+  constexpr int MFMAS = 4 * NB, READS = 4 + NB;   // a k-step
+  constexpr int WN = TN / 2, OUT_PITCH = WN + 4;
+  static_assert(4 * 32 * OUT_PITCH <= 2 * UNITS * 4);
+  using SideA = Side<TM, A_K>;
+  using SideB = Side<TN, B_K>;
+  __shared__ uint4 smem[2 * UNITS];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" ::: "a0");   // accumulators in AGPRs
+#endif
+  uint32_t tm, tn;
+  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(tm)) * TM;
+  const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(tn)) * TN;
+  SideA sa;
+  SideB sb;
+  sa.init(g.a, m0, g.m);
+  sb.init(g.b, n0, g.n);
+  const int nk = static_cast<int>((g.k + BK - 1) / BK);
+  const bool ragged = g.k % BK != 0;
+  const uint32_t wave_lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + wave * 64 * 16;
+  auto load_a = [&](int c, auto uc, auto checked) {
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(wave_lds + (c & 1) * (UNITS * 16));
+    sa.template load<decltype(uc)::value, decltype(checked)::value>(lds, static_cast<int64_t>(c) * BK,
+                                                                    g.k - static_cast<int64_t>(c) * BK);
+  };
+  auto load_b = [&](int c, auto uc, auto checked) {
+    const uint32_t lds = __builtin_amdgcn_readfirstlane(wave_lds + (c & 1) * (UNITS * 16) + A_UNITS * 16);
+    sb.template load<decltype(uc)::value, decltype(checked)::value>(lds, static_cast<int64_t>(c) * BK,
+                                                                    g.k - static_cast<int64_t>(c) * BK);
+  };
+  // The last stage's zeros, when it is in its slot.
+  auto pad = [&](int c) {
+    if (ragged && c == nk - 1) {
+      const int64_t left = g.k - static_cast<int64_t>(c) * BK;
+      SideA::zero(smem + (c & 1) * UNITS, left);
+      SideB::zero(smem + (c & 1) * UNITS + A_UNITS, left);
+      __syncthreads();
+    }
+  };
+
+  bf16x8 fa[2][4], fb[2][NB];
+  auto read_one = [&](int slot, int t, int buf, int q) {
+    const uint4* s = smem + slot * UNITS;
+    if (q < 4) fa[buf][q] = SideA::fragment(s, wm * 128 + q * 32, t, lane);
+    else fb[buf][q - 4] = SideB::fragment(s + A_UNITS, wn * WN + (q - 4) * 32, t, lane);
+  };
+  f32x16 acc[4][NB];
+  auto mfma1 = [&](int m, int buf) {
+    const int a = m / NB, b = m % NB;
+    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[buf][b], fa[buf][a], acc[a][b], 0, 0, 0);
+  };
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < NB; ++b) acc[a][b] = f32x16{};
+
+  static_for<SideA::LOADS>([&](auto uc) { load_a(0, uc, std::true_type{}); });
+  static_for<SideB::LOADS>([&](auto uc) { load_b(0, uc, std::true_type{}); });
+  if (nk > 1) {
+    static_for<SideA::LOADS>([&](auto uc) { load_a(1, uc, std::true_type{}); });
+    wait_vm<SideA::LOADS>();
+  } else {
+    wait_vm<0>();
+  }
+  __syncthreads();
+  pad(0);
+#pragma unroll
+  for (int q = 0; q < READS; ++q) read_one(0, 0, 0, q);
+  // Stage c; `last` where it may be one of the last three, whose coming stages
+  // do not exist or may be ragged.
+  auto stage = [&](int c, auto last) {
+    constexpr bool LAST = decltype(last)::value;
+    const int slot = c & 1;
+    // k-step 0: the next k-step's fragments and stage c+1's loads of B between
+    // the MFMAs; k-steps 1 and 2: the fragments of the next k-step.
+    const bool one = !LAST || c + 1 < nk, two = !LAST || c + 2 < nk;
+    static_for<MFMAS>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      mfma1(m, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (m < READS) read_one(slot, 1, 1, m);
+      if constexpr (m % 2 == 0) {
+        if (one) load_b(c + 1, std::integral_constant<int, m / 2>{}, last);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    static_for<2>([&](auto tc) {
+      constexpr int tt = decltype(tc)::value + 1;
+      static_for<MFMAS>([&](auto mc) {
+        constexpr int m = decltype(mc)::value;
+        mfma1(m, tt & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (m < READS) read_one(slot, tt + 1, (tt + 1) & 1, m);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+    // k-step 3: stage c+1 is whole, and this slot is free (every wave holds this
+    // k-step's fragments): the loads of A of stage c+2 and the fragments of
+    // stage c+1's k-step 0 between the MFMAs.
+    __builtin_amdgcn_sched_barrier(0);
+    if (one) {
+      wait_vm<0>();
+      __syncthreads();
+      if constexpr (LAST) pad(c + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int EVERY = MFMAS / SideA::LOADS;
+    static_for<MFMAS>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      mfma1(m, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (m % EVERY == 0) {
+        if (two) load_a(c + 2, std::integral_constant<int, m / EVERY>{}, last);
+      }
+      if constexpr (m < READS) {
+        if (one) read_one(slot ^ 1, 0, 0, m);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  };
+  int c = 0;
+  for (; c + 3 < nk; ++c) stage(c, std::false_type{});
+  for (; c < nk; ++c) stage(c, std::true_type{});
+
+  // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
+  // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS
+  // of its own, to leave in runs of 8: two per lane and turn, one copy of the code
+  // for all turns (unrolled, the epilogue was bound by the instruction cache's
+  // misses), the residual loaded three turns ahead.
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem) + wave * 32 * OUT_PITCH;
+  const int l32 = lane & 31, lh = lane >> 5;
+  constexpr int LANES = WN / 8, ROWS = 64 / LANES;   // lanes of a row, rows at a time
+  constexpr int TURNS = 32 / ROWS / 2;               // of a block
+  const Epilogue e = g.e;
+  const int64_t col = n0 + wn * WN + lane % LANES * 8;
+  const int64_t row0 = m0 + wm * 128 + lane / LANES;
+  float bias[8];
+  load_bias(e, col, g.n, bias);
+  auto epilogue = [&](auto checked_c) {
+    constexpr bool CHECKED = decltype(checked_c)::value;
+    RawRun ahead[3][2];
+    auto fetch = [&](int p, RawRun (&r)[2]) {
+      if (e.residual == nullptr || p >= 4 * TURNS) return;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = row0 + (2 * p + i) * ROWS;
+        if (!CHECKED || (row < g.m && col < g.n)) r[i] = load_raw<CHECKED>(e.residual, e.out_type, row, col, g.n);
+      }
+    };
+    static_for<3>([&](auto p) { fetch(decltype(p)::value, ahead[decltype(p)::value]); });
+#pragma unroll 1
+    for (int p = 0; p < 4 * TURNS; ++p) {
+      if (p % TURNS == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        static_for<4>([&](auto ac) {
+          constexpr int A = decltype(ac)::value;
+          if (p == A * TURNS) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(out + l32 * OUT_PITCH + b * 32 + q * 8 + lh * 4) =
+                    f32x4{acc[A][b][4 * q], acc[A][b][4 * q + 1], acc[A][b][4 * q + 2], acc[A][b][4 * q + 3]};
+            // (keeps the compiler from sinking the branches' common end, which would index the accumulators)
+            asm volatile("; block %0" ::"n"(A));
+          }
+        });
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      float z[2][8];
+      int64_t row[2];
+      bool ok[2];
+      RawRun res[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row[i] = row0 + (2 * p + i) * ROWS;
+        ok[i] = row[i] < g.m && col < g.n;
+        res[i] = ahead[0][i];
+        ahead[0][i] = ahead[1][i];
+        ahead[1][i] = ahead[2][i];
+        const int r = (2 * (p % TURNS) + i) * ROWS + lane / LANES;
+        __builtin_memcpy(z[i], __builtin_assume_aligned(out + r * OUT_PITCH + lane % LANES * 8, 16), 32);
+      }
+      fetch(p + 3, ahead[2]);
+      finish<2, CHECKED>(e, row, ok, col, g.n, bias, res, z);
+    }
+  };
+  if (m0 + TM <= g.m && n0 + TN <= g.n) epilogue(std::false_type{});
+  else epilogue(std::true_type{});
+}
+
+bool side_applies(const Operand& o, int64_t rows, int64_t k) {
+  // 16-byte loads at 32-bit offsets from a tile's first row
+  return reinterpret_cast<uintptr_t>(o.p) % 16 == 0 && (o.k_major ? rows : k) % 8 == 0 && o.ld < (int64_t{1} << 22);
+}
+
+}  // namespace
+
+bool wide_applies(const Product& g) {
+  return g.k > 0 && side_applies(g.a, g.m, g.k) && side_applies(g.b, g.n, g.k);
+}
+
+template <int TN>
+void launch_tn(const Product& g, unsigned grid, hipStream_t stream) {
+  if (!g.a.k_major && !g.b.k_major) wide_kernel<TN, false, false><<<grid, 256, 0, stream>>>(g);
+  else if (!g.a.k_major) wide_kernel<TN, false, true><<<grid, 256, 0, stream>>>(g);
+  else wide_kernel<TN, true, true><<<grid, 256, 0, stream>>>(g);
+}
+
+hipError_t launch_wide(Product g, int tn, hipStream_t stream) {
+  g.splits = 1;
+  g.tiles_m = static_cast<int32_t>((g.m + TM - 1) / TM);
+  g.tiles_n = static_cast<int32_t>((g.n + tn - 1) / tn);
+  const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(g.tiles_m) * g.tiles_n);
+  if (tn == 256) launch_tn<256>(g, grid, stream);
+  else launch_tn<128>(g, grid, stream);
+  return hipGetLastError();
+}
+
+}  // namespace vn

@@ -11,16 +11,22 @@ kernels of ``libvn.so``, asynchronously on the current stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
 
-from . import _lib, _ptr, _require_device, _stream
+from . import _lib, _require_device, _stream
 
 _ELEM = {torch.float32: _lib.VN_F32, torch.bfloat16: _lib.VN_BF16}
 _ACTIVATIONS = {None: _lib.VN_ACT_NONE, "none": _lib.VN_ACT_NONE, "relu": _lib.VN_ACT_RELU,
                 "gelu": _lib.VN_ACT_GELU, "silu": _lib.VN_ACT_SILU, "gelu_tanh": _lib.VN_ACT_GELU_TANH}
+
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
 
 
 def _elem(name: str, dtype: torch.dtype) -> int:
@@ -39,7 +45,8 @@ def _activation(activation: Optional[str]) -> int:
 
 def _aligned(t: torch.Tensor) -> torch.Tensor:
     """Dense and at a 16-byte address, as the matrix products load it."""
-    t = t.contiguous()
+    if not t.is_contiguous():
+        t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
@@ -49,7 +56,7 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, device) -> Optional[to
     _require_device(name, t, device)
     if t.shape != (n,):
         raise ValueError(f"{name} must be ({n},)")
-    return t.to(torch.float32).contiguous()
+    return t if t.dtype == torch.float32 and t.is_contiguous() else t.to(torch.float32).contiguous()
 
 
 def _output(name: str, out: Optional[torch.Tensor], shape, dtype: torch.dtype, device) -> torch.Tensor:
@@ -65,6 +72,19 @@ def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
     return torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes > 0 else None
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(name: str, *sizes: int) -> int:
+    """What the library's ``<name>_workspace_size`` says for these types and sizes (and nothing else)."""
+    name += "_workspace_size"
+    need = ctypes.c_int64(0)
+    _lib.check(name, getattr(_lib.load(), name)(*sizes, ctypes.byref(need)))
+    return need.value
+
+
+def _rows(shape: torch.Size) -> int:
+    return shape[0] if len(shape) == 2 else math.prod(shape[:-1])
+
+
 def _linear_operands(x: torch.Tensor, weight: torch.Tensor):
     _require_device("weight", weight)
     _require_device("x", x, weight.device)
@@ -74,7 +94,7 @@ def _linear_operands(x: torch.Tensor, weight: torch.Tensor):
         raise TypeError(f"x ({x.dtype}) and weight ({weight.dtype}) must share a dtype")
     if x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x and weight disagree on in_features")
-    return _elem("weight", weight.dtype), math.prod(x.shape[:-1])
+    return _elem("weight", weight.dtype), _rows(x.shape)
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -107,15 +127,14 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
         _require_device("residual", residual, dev)
         if residual.shape != shape or residual.dtype != out_dtype:
             raise ValueError(f"residual must be {tuple(shape)} in {out_dtype}")
-        r = residual.contiguous()
+        r = residual if residual.is_contiguous() else residual.contiguous()
     xc, wc = _aligned(x), _aligned(weight)
-    need = ctypes.c_int64(0)
-    _lib.check("vn_linear_workspace_size",
-               lib.vn_linear_workspace_size(kind, rows, in_f, out_f, ctypes.byref(need)))
-    ws = _workspace(need.value, dev)
-    st = lib.vn_linear(_ptr(xc), _ptr(wc), kind, _ptr(b), _ptr(r), rows, in_f, out_f, act, out_kind, _ptr(y),
-                       _ptr(pre), _ptr(ws), need.value, _stream(dev))
-    _lib.check("vn_linear", st)
+    need = _workspace_size("vn_linear", kind, rows, in_f, out_f)
+    ws = _workspace(need, dev)
+    st = lib.vn_linear(xc.data_ptr(), wc.data_ptr(), kind, _ptr(b), _ptr(r), rows, in_f, out_f, act, out_kind,
+                       y.data_ptr(), _ptr(pre), _ptr(ws), need, _stream(dev))
+    if st:
+        _lib.check("vn_linear", st)
     return y
 
 
@@ -155,15 +174,13 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
     dw = torch.empty(weight.shape, dtype=dw_dtype, device=dev) if weight_gradient else None
     db = torch.empty((out_f,), dtype=torch.float32, device=dev) if bias_gradient else None
-    need = ctypes.c_int64(0)
     wanted = (1 if input_gradient else 0) | (2 if weight_gradient else 0) | (4 if bias_gradient else 0)
-    _lib.check("vn_linear_backward_workspace_size",
-               lib.vn_linear_backward_workspace_size(kind, dy_kind, rows, in_f, out_f, act, wanted,
-                                                     ctypes.byref(need)))
-    ws = _workspace(need.value, dev)
-    st = lib.vn_linear_backward(_ptr(dyc), dy_kind, _ptr(xc), _ptr(wc), kind, _ptr(z), rows, in_f, out_f, act,
-                                _ptr(dx), _ptr(dw), dw_kind, _ptr(db), _ptr(ws), need.value, _stream(dev))
-    _lib.check("vn_linear_backward", st)
+    need = _workspace_size("vn_linear_backward", kind, dy_kind, rows, in_f, out_f, act, wanted)
+    ws = _workspace(need, dev)
+    st = lib.vn_linear_backward(dyc.data_ptr(), dy_kind, xc.data_ptr(), wc.data_ptr(), kind, _ptr(z), rows, in_f,
+                                out_f, act, _ptr(dx), _ptr(dw), dw_kind, _ptr(db), _ptr(ws), need, _stream(dev))
+    if st:
+        _lib.check("vn_linear_backward", st)
     return dx, dw, db
 
 
@@ -188,11 +205,12 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     out_kind = _elem("out", out_dtype)
     y = _output("out", out, x.shape, out_dtype, dev)
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
-    xc = x.contiguous()
-    st = lib.vn_layer_norm(_ptr(xc), kind, _ptr(w), _ptr(b), math.prod(x.shape[:-1]), n, float(eps), _ptr(y),
-                           out_kind, _ptr(mean), _ptr(rstd), _stream(dev))
-    _lib.check("vn_layer_norm", st)
+    rstd = torch.empty_like(mean) if stats else None
+    xc = x if x.is_contiguous() else x.contiguous()
+    st = lib.vn_layer_norm(xc.data_ptr(), kind, _ptr(w), _ptr(b), _rows(x.shape), n, eps, y.data_ptr(), out_kind,
+                           _ptr(mean), _ptr(rstd), _stream(dev))
+    if st:
+        _lib.check("vn_layer_norm", st)
     return (y, mean, rstd) if stats else y
 
 
@@ -211,7 +229,7 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     if x.dim() < 1:
         raise ValueError("x must have a last axis to normalise")
     n = x.shape[-1]
-    rows = math.prod(x.shape[:-1])
+    rows = _rows(x.shape)
     kind = _elem("x", x.dtype)
     _require_device("dy", dy, dev)
     if dy.shape != x.shape:
@@ -223,20 +241,19 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
             raise ValueError(f"{name} must be {tuple(x.shape[:-1])} in float32")
     w = _vector("weight", weight, n, dev)
     dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
-    sums = torch.empty((2, n), dtype=torch.float32, device=dev) if parameter_gradients else None
-    dw, db = (sums[0], sums[1]) if parameter_gradients else (None, None)
-    need = ctypes.c_int64(0)
-    if parameter_gradients:
-        _lib.check("vn_layer_norm_backward_workspace_size",
-                   lib.vn_layer_norm_backward_workspace_size(rows, n, ctypes.byref(need)))
-    ws = _workspace(need.value, dev)
+    dw = torch.empty((n,), dtype=torch.float32, device=dev) if parameter_gradients else None
+    db = torch.empty_like(dw) if parameter_gradients else None
+    need = _workspace_size("vn_layer_norm_backward", rows, n) if parameter_gradients else 0
+    ws = _workspace(need, dev)
     dyc, xc, mc, rc = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
-    st = lib.vn_layer_norm_backward(_ptr(dyc), dy_kind, _ptr(xc), kind, _ptr(w), _ptr(mc), _ptr(rc), rows, n,
-                                    _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need.value, _stream(dev))
-    _lib.check("vn_layer_norm_backward", st)
+    st = lib.vn_layer_norm_backward(dyc.data_ptr(), dy_kind, xc.data_ptr(), kind, _ptr(w), mc.data_ptr(),
+                                    rc.data_ptr(), rows, n, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, _stream(dev))
+    if st:
+        _lib.check("vn_layer_norm_backward", st)
     return dx, dw, db
 
 
+_DATA_PTR = torch.Tensor.data_ptr
 _BLOCK = 128   # state elements that share a scale; tensors start at whole blocks
 
 
@@ -367,7 +384,7 @@ class AdamW:
         if lr is not None:
             self.lr = float(lr)
         # a tensor that was given other memory since: its old memory is not written
-        if [t.data_ptr() for t in self._checked] != self._bound or [g.data_ptr() for g in self.grads] != self._grad_bound:
+        if list(map(_DATA_PTR, self._checked)) != self._bound or list(map(_DATA_PTR, self.grads)) != self._grad_bound:
             raise ValueError("a parameter, copy or gradient has been given other memory: make a new AdamW with state=")
         lib, s = self._lib, self.state
         stream = _stream(self.device)
