@@ -45,10 +45,11 @@ def test_linear_validation(lib):
         assert linear(lib, **{name: None}) == E.VN_ERR_NULL
     for name in ("x", "w", "y", "b", "r", "pre", "ws"):
         assert linear(lib, **{name: ODD}) == E.VN_ERR_ALIGN
-    st, need = size_of(lib.vn_linear_workspace_size, E.VN_F32, 1000, 1000, 1000)
+    # (a size whose few tiles share out k, with partial sums in the workspace)
+    st, need = size_of(lib.vn_linear_workspace_size, E.VN_F32, 100, 4096, 100)
     assert st == E.VN_OK and need > 0
-    assert linear(lib, rows=1000, i=1000, o=1000, wsb=need - 1) == E.VN_ERR_SHAPE
-    assert linear(lib, rows=1000, i=1000, o=1000, ws=None, wsb=need) == E.VN_ERR_NULL
+    assert linear(lib, rows=100, i=4096, o=100, wsb=need - 1) == E.VN_ERR_SHAPE
+    assert linear(lib, rows=100, i=4096, o=100, ws=None, wsb=need) == E.VN_ERR_NULL
     # nothing to write
     assert linear(lib, rows=0, x=None, y=None) == E.VN_OK
     assert linear(lib, o=0, w=None, y=None) == E.VN_OK

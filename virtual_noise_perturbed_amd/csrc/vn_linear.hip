@@ -31,25 +31,24 @@ template <int SEGS> __device__ __forceinline__ int swz(int r) {
   else return ((r >> 1) & 3) ^ ((r >> 3) & 1);
 }
 
-// 8 values as the units of their planes.
-__device__ __forceinline__ void split_planes(const float (&v)[8], uint4 (&u)[3]) {
-  uint32_t w[3][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = v[2 * i], b = v[2 * i + 1];
-    // (the largest finite values would round up to infinity: their plane h is
-    // the largest bf16, and m takes the rest)
-    constexpr float kMost = 0x1.FEp127f;
-    w[0][i] = pack_bf16(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost));
-    a -= __builtin_bit_cast(float, w[0][i] << 16);
-    b -= __builtin_bit_cast(float, w[0][i] & 0xFFFF0000u);
-    w[1][i] = pack_bf16(a, b);
-    a -= __builtin_bit_cast(float, w[1][i] << 16);
-    b -= __builtin_bit_cast(float, w[1][i] & 0xFFFF0000u);
-    w[2][i] = pack_bf16(a, b);
-  }
-#pragma unroll
-  for (int q = 0; q < 3; ++q) u[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+// What a pair of values leaves beside a plane's pair w, exactly.  (As a
+// v_dot2_f32_bf16 each it is half the instructions, but no faster: 127 us against
+// 120 in the 2048^3 product.)
+__device__ __forceinline__ void leave(uint32_t w, float& a, float& b) {
+  a -= __builtin_bit_cast(float, w << 16);
+  b -= __builtin_bit_cast(float, w & 0xFFFF0000u);
+}
+
+// A pair of values as pairs of their planes.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t& h, uint32_t& m, uint32_t& l) {
+  // (the largest finite values would round up to infinity: their plane h is the
+  // largest bf16, and m takes the rest)
+  constexpr float kMost = 0x1.FEp127f;
+  h = pack_bf16(__builtin_amdgcn_fmed3f(a, -kMost, kMost), __builtin_amdgcn_fmed3f(b, -kMost, kMost));
+  leave(h, a, b);
+  m = pack_bf16(a, b);
+  leave(m, a, b);
+  l = pack_bf16(a, b);
 }
 
 // C consecutive elements at any element-aligned address, as they lie in memory.
@@ -76,52 +75,55 @@ template <typename T, int C> __device__ __forceinline__ Few<T, C> load_few(const
 // Rows past the end are read from the last row (k-major: from what follows in
 // memory, inside the matrix); they reach only outputs that are not stored.
 // k past the end is zero.
-template <typename T, int ROWS>
+template <typename T, int ROWS, bool K_MAJOR>
 struct Staged {
-  static constexpr int SEGS = Kind<T>::BK / 8;
+  static constexpr int PLANES = Kind<T>::PLANES, SEGS = Kind<T>::BK / 8;
   static constexpr int UNITS = ROWS * SEGS / 256;
   static constexpr int STRIDE = 256 / SEGS;   // threads side by side
-  union {
-    Run8<T> run[UNITS];
-    Few<T, UNITS> few[8];
-  };
+  static constexpr int STEPS = UNITS * 2;     // of the way to LDS: two pairs of k each
+  Run8<T> run[K_MAJOR ? 1 : UNITS];
+  Few<T, UNITS> few[K_MAJOR ? 8 : 1];
+  uint32_t w[PLANES][4];                      // the unit under way
+  // this thread's first elements at k = 0: of each row, or of its first k
+  const T* at[K_MAJOR ? 1 : UNITS];
 
-  // Whether the stage at k can be loaded without checks: all its k exist and,
-  // k-major, what the threads of the last row read past it lies in later k's.
-  static __device__ __forceinline__ bool whole(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
-    return k + Kind<T>::BK <= kn && (!o.k_major || r0 + ROWS <= rows || k + Kind<T>::BK + UNITS <= kn);
-  }
-
-  __device__ __forceinline__ void load(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
+  __device__ __forceinline__ void init(const Operand& o, int64_t r0, int64_t rows) {
     const T* p = static_cast<const T*>(o.p);
     const int tid = threadIdx.x;
-    if (!o.k_major) {
-      const int64_t kk = k + tid % SEGS * 8;
+    if constexpr (!K_MAJOR) {
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
         const int64_t r = r0 + u * STRIDE + tid / SEGS;
-        const T* row = p + (r < rows ? r : rows - 1) * o.ld;
-        __builtin_memcpy(&run[u], row + kk, sizeof(run[u]));
+        at[u] = p + (r < rows ? r : rows - 1) * o.ld + tid % SEGS * 8;
       }
     } else {
-      const int64_t kk = k + tid / STRIDE * 8;
       const int64_t c = r0 + tid % STRIDE * UNITS;
-      const T* col = p + kk * o.ld + (c < rows ? c : rows - 1);
+      at[0] = p + tid / STRIDE * 8 * o.ld + (c < rows ? c : rows - 1);
+    }
+  }
+
+  // The last k whose stage can be loaded without checks: all its k exist and,
+  // k-major, what the threads of the last row read past it lies in later k's.
+  static __device__ __forceinline__ int64_t last_whole(int64_t r0, int64_t rows, int64_t kn) {
+    return kn - Kind<T>::BK - (K_MAJOR && r0 + ROWS > rows ? UNITS : 0);
+  }
+  __device__ __forceinline__ void load(const Operand& o, int64_t k) {
+    if constexpr (!K_MAJOR) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) __builtin_memcpy(&run[u], at[u] + k, sizeof(run[u]));
+    } else {
+      const T* col = at[0] + k * o.ld;
 #pragma unroll
       for (int i = 0; i < 8; ++i) few[i] = load_few<T, UNITS>(col + i * o.ld);
     }
   }
   // The same with every element checked.
   __device__ __forceinline__ void load_checked(const Operand& o, int64_t r0, int64_t rows, int64_t k, int64_t kn) {
-    const T* p = static_cast<const T*>(o.p);
     const int tid = threadIdx.x;
-    if (!o.k_major) {
-      const int64_t kk = k + tid % SEGS * 8;
+    if constexpr (!K_MAJOR) {
+      const int64_t kk = tid % SEGS * 8;
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int64_t r = r0 + u * STRIDE + tid / SEGS;
-        run[u] = load_run(p + (r < rows ? r : rows - 1) * o.ld, kk, kn);
-      }
+      for (int u = 0; u < UNITS; ++u) run[u] = load_run(at[u] - kk, k + kk, kn);
     } else {
       const int64_t kk = k + tid / STRIDE * 8;
       const int64_t c = r0 + tid % STRIDE * UNITS;
@@ -129,72 +131,74 @@ struct Staged {
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < UNITS; ++j)
-          few[i].e[j] = kk + i < kn && c + j < rows ? p[(kk + i) * o.ld + c + j] : static_cast<T>(0.0f);
+          few[i].e[j] = kk + i < kn && c + j < rows ? static_cast<const T*>(o.p)[(kk + i) * o.ld + c + j]
+                                                    : static_cast<T>(0.0f);
     }
   }
 
-  __device__ __forceinline__ void store_unit(uint4* lds, int r, int s, const float (&v)[8]) const {
-    uint4 u[3];
-    split_planes(v, u);
-#pragma unroll
-    for (int q = 0; q < 3; ++q) lds[q * ROWS * SEGS + r * SEGS + (s ^ swz<SEGS>(r))] = u[q];
-  }
-  __device__ __forceinline__ void store(const Operand& o, uint4* lds) const {
-    const int tid = threadIdx.x;
-    if (!o.k_major) {
-      const int s = tid % SEGS;
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int r = u * STRIDE + tid / SEGS;
-        if constexpr (sizeof(T) == 4) {
-          float v[8];
-          run_values(run[u], v);
-          store_unit(lds, r, s, v);
-        } else {
-          uint4 w;
-          __builtin_memcpy(&w, &run[u], 16);
-          lds[r * SEGS + (s ^ swz<SEGS>(r))] = w;
-        }
+  // Pair I of unit U as pairs of its planes.
+  template <int U, int I>
+  __device__ __forceinline__ void pair() {
+    if constexpr (sizeof(T) == 4) {
+      float a, b;
+      if constexpr (!K_MAJOR) {
+        const u32x4_any& v = I < 2 ? run[U].a : run[U].b;
+        a = __builtin_bit_cast(float, static_cast<uint32_t>(v[I % 2 * 2]));
+        b = __builtin_bit_cast(float, static_cast<uint32_t>(v[I % 2 * 2 + 1]));
+      } else {
+        a = few[2 * I].e[U];
+        b = few[2 * I + 1].e[U];
       }
+      split_pair(a, b, w[0][I], w[1][I], w[2][I]);
+    } else if constexpr (!K_MAJOR) {
+      w[0][I] = run[U].a[I];
     } else {
-      const int s = tid / STRIDE;
+      w[0][I] = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * I].e[U])) |
+                static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * I + 1].e[U])) << 16;
+    }
+  }
+  // Step J of the way to the slot at `lds`: half of unit J / 2, whose planes are
+  // stored with the second half.
+  template <int J>
+  __device__ __forceinline__ void step(uint4* lds) {
+    constexpr int U = J / 2, I = J % 2 * 2;
+    const int tid = threadIdx.x;
+    pair<U, I>();
+    pair<U, I + 1>();
+    if constexpr (I == 2) {
+      const int r = K_MAJOR ? tid % STRIDE * UNITS + U : U * STRIDE + tid / SEGS;
+      const int s = K_MAJOR ? tid / STRIDE : tid % SEGS;
 #pragma unroll
-      for (int j = 0; j < UNITS; ++j) {
-        const int r = tid % STRIDE * UNITS + j;
-        if constexpr (sizeof(T) == 4) {
-          float v[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = few[i].e[j];
-          store_unit(lds, r, s, v);
-        } else {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            w[i] = static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * i].e[j])) |
-                   static_cast<uint32_t>(__builtin_bit_cast(uint16_t, few[2 * i + 1].e[j])) << 16;
-          lds[r * SEGS + (s ^ swz<SEGS>(r))] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
+      for (int q = 0; q < PLANES; ++q)
+        lds[q * ROWS * SEGS + r * SEGS + (s ^ swz<SEGS>(r))] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
     }
   }
 };
 
-// One tile of TM x TN outputs by 4 waves (2 x 2), over one split of k.  A stage
-// waits in registers while the one before it is multiplied out of LDS.  The
-// matrix cores get B's rows first, so that a lane holds 4 neighbouring columns of
+// One tile of TM x TN outputs by 4 waves (2 x 2), over one split of k.  Two LDS
+// slots: while a stage is multiplied out of one, the next is split into its
+// planes and stored to the other, a pair of values after each MFMA or two, and
+// the one after that is on its way into registers; one barrier a stage, before the
+// last k-step, whose MFMAs cover the next stage's first fragment reads.  (Split and
+// multiplied in turn, with the overlap left to two workgroups a CU, the two kept
+// step with each other and took the sum of both: 3570 cycles for a 128 x 128 x 32
+// stage in fp32 whose MFMAs take 1536.)
+// The matrix cores get B's rows first, so that a lane holds 4 neighbouring columns of
 // an output row; the outputs pass through LDS once more to leave in runs of 8.
-template <typename T, int TM, int TN>
-__global__ __launch_bounds__(256, 2) void tile_kernel(Products gs) {
-  constexpr int BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES;
+template <typename T, int TM, int TN, bool A_K, bool B_K>
+__device__ __forceinline__ void tile_body(const Product& g, uint4* smem) {
+  constexpr int BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES, STEPS_K = BK / 16;
   constexpr int WM = TM / 2, WN = TN / 2, MB = WM / 32, NB = WN / 32;
-  constexpr int A_UNITS = PLANES * TM * SEGS, B_UNITS = PLANES * TN * SEGS;
+  constexpr int A_UNITS = PLANES * TM * SEGS, SLOT = A_UNITS + PLANES * TN * SEGS;
+  constexpr int TERMS = PLANES == 3 ? 6 : 1, MFMAS = TERMS * MB * NB;   // a k-step
+  constexpr int READS = PLANES * (MB + NB);
   constexpr int OUT_PITCH = WN + 4;   // floats: rows of 16-byte writes spread over the banks
-  constexpr int OUT_UNITS = 4 * 32 * OUT_PITCH / 4;
-  __shared__ uint4 smem[A_UNITS + B_UNITS > OUT_UNITS ? A_UNITS + B_UNITS : OUT_UNITS];
+  static_assert(4 * 32 * OUT_PITCH <= 2 * SLOT * 4);
+  using SA = Staged<T, TM, A_K>;
+  using SB = Staged<T, TN, B_K>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
-  const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
   const uint32_t tiles = static_cast<uint32_t>(g.tiles_m) * g.tiles_n;
   const uint32_t id = blockIdx.x - g.first, split = id / tiles;
   uint32_t tm, tn;
@@ -205,62 +209,127 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Products gs) {
   const int64_t begin = split * per * BK;
   const int64_t end = (split + 1) * per * BK < stages * BK ? (split + 1) * per * BK : stages * BK;
 
-  Staged<T, TM> sa;
-  Staged<T, TN> sb;
-  auto load = [&](int64_t k) {
-    if (Staged<T, TM>::whole(g.a, m0, g.m, k, g.k)) sa.load(g.a, m0, g.m, k, g.k);
-    else sa.load_checked(g.a, m0, g.m, k, g.k);
-    if (Staged<T, TN>::whole(g.b, n0, g.n, k, g.k)) sb.load(g.b, n0, g.n, k, g.k);
-    else sb.load_checked(g.b, n0, g.n, k, g.k);
+  // The stages that load without checks go through the pipeline; those that do
+  // not, the last two at most, come after it one by one.
+  const int64_t last = SA::last_whole(m0, g.m, g.k) < SB::last_whole(n0, g.n, g.k) ? SA::last_whole(m0, g.m, g.k)
+                                                                                   : SB::last_whole(n0, g.n, g.k);
+  const int64_t run_to = last < begin ? begin : begin + ((last - begin) / BK + 1) * BK;
+  const int64_t whole = run_to < end ? run_to : end;
+
+  SA sa[2];   // stages of even and of odd number
+  SB sb[2];
+  sa[0].init(g.a, m0, g.m);
+  sb[0].init(g.b, n0, g.n);
+  sa[1].init(g.a, m0, g.m);
+  sb[1].init(g.b, n0, g.n);
+  auto load = [&](int64_t k, auto pc) {
+    constexpr int P = decltype(pc)::value;
+    if (k >= whole) return;
+    sa[P].load(g.a, k);
+    sb[P].load(g.b, k);
+  };
+  // Steps of a stage's way from the registers to its slot; EARLY of them go
+  // between the last k-step's MFMAs of the stage two before it.
+  constexpr int STEPS = SA::STEPS + SB::STEPS, EARLY = STEPS / STEPS_K;
+  auto step = [&](auto jc, auto pc, uint4* slot) {
+    constexpr int J = decltype(jc)::value, P = decltype(pc)::value;
+    if constexpr (J < SA::STEPS) sa[P].template step<J>(slot);
+    else sb[P].template step<J - SA::STEPS>(slot + A_UNITS);
   };
 
   const int l32 = lane & 31, lh = lane >> 5;
   const int swl = swz<SEGS>(l32);
   const int arow = (wm * WM + l32) * SEGS;
   const int brow = A_UNITS + (wn * WN + l32) * SEGS;
+  bf16x8 fa[2][PLANES][MB], fb[2][PLANES][NB];
+  // Read Q of a k-step's fragments, plane by plane as the products need them.
+  auto read = [&](const uint4* slot, int t, auto bufc, auto qc) {
+    constexpr int BUF = decltype(bufc)::value, Q = decltype(qc)::value;
+    constexpr int plane = Q / (MB + NB), x = Q % (MB + NB);
+    const int seg = (2 * t + lh) ^ swl;
+    if constexpr (x < MB)
+      fa[BUF][plane][x] = __builtin_bit_cast(bf16x8, slot[plane * TM * SEGS + arow + x * 32 * SEGS + seg]);
+    else
+      fb[BUF][plane][x - MB] =
+          __builtin_bit_cast(bf16x8, slot[plane * TN * SEGS + brow + (x - MB) * 32 * SEGS + seg]);
+  };
   f32x16 acc[MB][NB];
 #pragma unroll
   for (int a = 0; a < MB; ++a)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[a][b] = f32x16{};
+  // MFMA M of a k-step; the planes' products smallest first.
+  auto mfma = [&](auto mc, auto bufc) {
+    constexpr int M = decltype(mc)::value, BUF = decltype(bufc)::value;
+    constexpr int term = M / (MB * NB), a = M / NB % MB, b = M % NB;
+    constexpr int pa = PLANES == 3 ? (term == 0 ? 2 : term == 1 || term == 3 ? 1 : 0) : 0;
+    constexpr int pb = PLANES == 3 ? (term == 2 ? 2 : term == 1 || term == 4 ? 1 : 0) : 0;
+    acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[BUF][pb][b], fa[BUF][pa][a], acc[a][b], 0, 0, 0);
+  };
 
-  if (begin < end) load(begin);
-  for (int64_t k = begin; k < end; k += BK) {
-    __syncthreads();   // the stage before is multiplied
-    sa.store(g.a, smem);
-    sb.store(g.b, smem + A_UNITS);
-    if (k + BK < end) load(k + BK);
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  uint4* const slots[2] = {smem, smem + SLOT};
+  if (begin < whole) {
+    load(begin, even);
+    load(begin + BK, odd);
+    static_for<STEPS>([&](auto jc) { step(jc, even, slots[0]); });
+    load(begin + 2 * BK, even);
+    static_for<EARLY>([&](auto jc) { step(jc, odd, slots[1]); });
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < BK / 16; ++t) {
-      const int seg = (2 * t + lh) ^ swl;
-      bf16x8 fa[PLANES][MB], fb[PLANES][NB];
-#pragma unroll
-      for (int q = 0; q < PLANES; ++q) {
-#pragma unroll
-        for (int a = 0; a < MB; ++a)
-          fa[q][a] = __builtin_bit_cast(bf16x8, smem[q * TM * SEGS + arow + a * 32 * SEGS + seg]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          fb[q][b] = __builtin_bit_cast(bf16x8, smem[q * TN * SEGS + brow + b * 32 * SEGS + seg]);
-      }
-      auto multiply = [&](int p, int q) {
-#pragma unroll
-        for (int a = 0; a < MB; ++a)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q][b], fa[p][a], acc[a][b], 0, 0, 0);
-      };
-      if constexpr (PLANES == 3) {   // smallest first
-        multiply(2, 0);
-        multiply(1, 1);
-        multiply(0, 2);
-        multiply(1, 0);
-        multiply(0, 1);
-      }
-      multiply(0, 0);
-    }
+    static_for<READS>([&](auto qc) { read(slots[0], 0, std::integral_constant<int, 0>{}, qc); });
   }
+  // The stage at k, of parity P.  (Past the last stage, what is stored to the slots
+  // and read from them is not used.)
+  auto stage = [&](int64_t k, auto pc) {
+    constexpr int P = decltype(pc)::value;
+    constexpr std::integral_constant<int, P ^ 1> other{};
+    static_for<STEPS_K>([&](auto tc) {
+      constexpr int t = decltype(tc)::value;
+      constexpr bool LAST = t == STEPS_K - 1;
+      if constexpr (LAST) {
+        __builtin_amdgcn_sched_barrier(0);
+        load(k + 3 * BK, other);
+        __syncthreads();   // the next stage is whole; this one's fragments are in registers
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      static_for<MFMAS>([&](auto mc) {
+        constexpr int m = decltype(mc)::value;
+        mfma(mc, std::integral_constant<int, t & 1>{});
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<READS>([&](auto qc) {
+          if constexpr ((decltype(qc)::value < MFMAS ? decltype(qc)::value : MFMAS - 1) == m) {
+            if constexpr (LAST) read(slots[P ^ 1], 0, std::integral_constant<int, 0>{}, qc);
+            else read(slots[P], t + 1, std::integral_constant<int, (t + 1) & 1>{}, qc);
+          }
+        });
+        static_for<STEPS>([&](auto jc) {
+          constexpr int J = decltype(jc)::value;
+          if constexpr (LAST && J < EARLY && J * MFMAS / EARLY == m) step(jc, pc, slots[P]);
+          if constexpr (!LAST && J >= EARLY && (J - EARLY) * (STEPS_K - 1) * MFMAS / (STEPS - EARLY) == t * MFMAS + m)
+            step(jc, other, slots[P ^ 1]);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+  };
+  for (int64_t k = begin; k < whole; k += 2 * BK) {
+    stage(k, even);
+    if (k + BK < whole) stage(k + BK, odd);
+  }
+#pragma unroll 1
+  for (int64_t k = whole; k < end; k += BK) {
+    sa[0].load_checked(g.a, m0, g.m, k, g.k);
+    sb[0].load_checked(g.b, n0, g.n, k, g.k);
+    __syncthreads();
+    static_for<STEPS>([&](auto jc) { step(jc, even, slots[0]); });
+    __syncthreads();
+    static_for<STEPS_K>([&](auto tc) {
+      static_for<READS>([&](auto qc) { read(slots[0], decltype(tc)::value, even, qc); });
+      static_for<MFMAS>([&](auto mc) { mfma(mc, even); });
+    });
+  }
+  static_assert(STEPS_K % 2 == 0);   // (a stage's first fragments are in buffer 0)
 
   // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
   // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS of
@@ -324,6 +393,31 @@ __global__ __launch_bounds__(256, 2) void tile_kernel(Products gs) {
   else epilogue(std::true_type{});
 }
 
+template <typename T, int TM, int TN>
+constexpr int smem_units() {
+  return 2 * Kind<T>::PLANES * (TM + TN) * (Kind<T>::BK / 8);
+}
+template <typename T, int T_>
+constexpr int per_cu() {   // workgroups: LDS allows so many, and their registers
+  return T_ == 64 ? 3 : sizeof(T) == 4 ? 1 : 2;
+}
+
+// The forward's product.
+template <typename T, int TILE>
+__global__ __launch_bounds__(256, (per_cu<T, TILE>())) void tile_kernel(Product g) {
+  __shared__ uint4 smem[smem_units<T, TILE, TILE>()];
+  tile_body<T, TILE, TILE, false, false>(g, smem);
+}
+
+// The gradients' products, one or both.
+template <typename T, int TILE>
+__global__ __launch_bounds__(256, (per_cu<T, TILE>())) void gradient_kernel(Products gs) {
+  __shared__ uint4 smem[smem_units<T, TILE, TILE>()];
+  const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
+  if (g.a.k_major) tile_body<T, TILE, TILE, true, true>(g, smem);
+  else tile_body<T, TILE, TILE, false, true>(g, smem);
+}
+
 // ---- what follows a product ------------------------------------------------
 
 // Joins of splits' partial products, in split order, and of the bias gradient's
@@ -350,8 +444,18 @@ __global__ __launch_bounds__(256) void join_kernel(Joins j) {
       const int64_t per = (j.parts + 3) / 4;
       const int64_t end = (wave + 1) * per < j.parts ? (wave + 1) * per : j.parts;
       float t = 0.0f;
-      if (c < j.n)
-        for (int64_t k = wave * per; k < end; ++k) t += j.sums[k * j.n + c];
+      if (c < j.n) {
+        // (8 loads on their way at a time)
+        int64_t k = wave * per;
+        for (; k + 8 <= end; k += 8) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = j.sums[(k + i) * j.n + c];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t += v[i];
+        }
+        for (; k < end; ++k) t += j.sums[k * j.n + c];
+      }
       s[threadIdx.x] = t;
       __syncthreads();
       if (wave == 0 && c < j.n) j.db[c] = ((s[lane] + s[lane + 64]) + s[lane + 128]) + s[lane + 192];
@@ -376,7 +480,7 @@ __global__ __launch_bounds__(256) void join_kernel(Joins j) {
   finish<1, true>(g.e, {m}, {true}, c, g.n, bias, res, z);
 }
 
-// dz = dy act'(pre), as the products take it, and sums of its columns over 64
+// dz = dy act'(pre), as the products take it, and sums of its columns over `span`
 // rows each: 256 columns per workgroup, 8 a thread, 8 rows at a time.
 struct Slope {
   const void* dy;
@@ -386,7 +490,8 @@ struct Slope {
   Act act;
   int64_t rows, n;
   void* dz;              // or null
-  float* sums;           // (ceil(rows / 64), n), or null
+  float* sums;           // (ceil(rows / span), n), or null
+  int32_t span;          // rows of a workgroup, a multiple of 8
 };
 
 __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
@@ -396,9 +501,9 @@ __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
   const int64_t part = blockIdx.x / ct, c = (blockIdx.x % ct) * 256 + seg * 8;
   float sum[8] = {};
   if (c < p.n) {
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = part * 64 + i * 8 + group;
+#pragma unroll 2
+    for (int i = group; i < p.span; i += 8) {
+      const int64_t r = part * p.span + i;
       if (r < p.rows) {
         float v[8];
         raw_values(load_raw<true>(p.dy, p.dy_type, r, c, p.n), p.dy_type, v);
@@ -451,15 +556,16 @@ int plan(Products& gs, Elem type, Arena& ws) {
   int64_t work[2] = {0, 0};   // stages of all tiles of 64, of 128
   for (int i = 0; i < gs.count; ++i)
     for (int t = 0; t < 2; ++t) work[t] += tiles_of(gs.g[i], 64 << t) * ((gs.g[i].k + bk - 1) / bk);
-  // Tiles of 128 where every one of the 512 that the card holds gets 16 stages:
-  // 2048^3 in fp32 takes 115 us on them, 140 on tiles of 64; 777 x 1024 x 1000's
-  // gradients 50 and 47.
-  const int tile = work[1] >= 512 * 16 ? 128 : 64;
-  const int64_t total = work[tile / 128], slots = tile == 128 ? 512 : 1024;
-  // A workgroup's stages: an equal share of all, but enough to repay a split's
-  // partial sums and their join (1000^3 in bf16: 16 us whole, 22 us in splits of 4).
-  const int64_t least = type == Elem::f32 ? 5 : 8;
-  const int64_t share = total / slots < least ? least : total / slots;
+  // Tiles of 128 where each CU gets 32 of their stages: 2048^3 in fp32 takes
+  // 113 us on them, 144 on tiles of 64; 4000 x 700 x 700 41 and 36 us.
+  const int tile = work[1] >= 256 * 32 ? 128 : 64;
+  // A workgroup's stages: an equal share of all for each CU (with two products, half
+  // of it, as theirs differ), but enough to repay a split's partial sums and their
+  // join.  fp32, 2011 x 784 x 256: 20.5 us whole, 17.4 in 2 splits, 18.3 in 4;
+  // 200 x 300 x 100: 10.2 whole, 9.2 in 3.  bf16, 1000^3: 10.1 whole, 16.8 in 2.
+  const int64_t least = type == Elem::f32 ? 3 : 8;
+  const int64_t each = gs.count > 0 ? work[tile / 128] / (256 * gs.count) : 0;
+  const int64_t share = each < least ? least : each;
   uint32_t first = 0;
   for (int i = 0; i < gs.count; ++i) {
     Product& g = gs.g[i];
@@ -478,8 +584,13 @@ int plan(Products& gs, Elem type, Arena& ws) {
 
 template <typename T>
 void launch_tiles(const Products& gs, int tile, unsigned blocks, hipStream_t stream) {
-  if (tile == 128) tile_kernel<T, 128, 128><<<blocks, 256, 0, stream>>>(gs);
-  else tile_kernel<T, 64, 64><<<blocks, 256, 0, stream>>>(gs);
+  if (!gs.g[0].b.k_major) {
+    if (tile == 128) tile_kernel<T, 128><<<blocks, 256, 0, stream>>>(gs.g[0]);
+    else tile_kernel<T, 64><<<blocks, 256, 0, stream>>>(gs.g[0]);
+  } else {
+    if (tile == 128) gradient_kernel<T, 128><<<blocks, 256, 0, stream>>>(gs);
+    else gradient_kernel<T, 64><<<blocks, 256, 0, stream>>>(gs);
+  }
 }
 
 // The width of the wide tiles for a product, or 0: the tiles of `plan`.  What a
@@ -561,8 +672,11 @@ hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need
   // dz is dy itself where that serves
   const bool plain = p.act == Act::none && p.dy_type == p.type;
   const bool need_dz = !plain && (need_dx || need_dw) && p.rows > 0 && p.out > 0;
-  const int64_t parts = (p.rows + 63) / 64;
-  Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr};
+  // 64 rows a workgroup, or fewer where those would leave CUs idle
+  int span = 64;
+  while (span > 8 && (p.rows + span - 1) / span * ((p.out + 255) / 256) < 512) span /= 2;
+  const int64_t parts = (p.rows + span - 1) / span;
+  Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr, span};
   if (need_dz) z.dz = ws.take<char>(p.rows * p.out * size);
   if (need_db) z.sums = ws.take<float>(parts * p.out * 4);
   Products gs{};
