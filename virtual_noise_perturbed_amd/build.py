@@ -19,8 +19,8 @@ LIB = os.path.join(PKG, "libvn.so")
 PROBE = os.path.join(PKG, "vn_probe")
 ARCH = "gfx950"
 
-SOURCES = ["vn_kernels.hip", "vn_gemm.hip", "vn_norm.hip", "vn_adamw.hip", "vn_linear.hip", "vn_linear_wide.hip", "vn_api.cpp",
-           "vn_dense_api.cpp"]
+SOURCES = ["vn_kernels.hip", "vn_gemm.hip", "vn_norm.hip", "vn_adamw.hip", "vn_linear.hip", "vn_linear_wide.hip",
+           "vn_linear_few.hip", "vn_api.cpp", "vn_dense_api.cpp"]
 
 HIPCC_FLAGS = [
     f"--offload-arch={ARCH}",

@@ -655,6 +655,7 @@ hipError_t linear_steps(const LinearParams& p, Arena& ws, hipStream_t stream) {
   g.n = p.out;
   g.k = p.in;
   g.e = {p.bias, p.residual, p.act, p.out_type, p.type, p.y, p.pre};
+  if (few_applies(g)) return ws.base != nullptr ? launch_few(g, p.type, stream) : hipSuccess;
   const hipError_t err = run_wide(gs, p.type, ws.base != nullptr, stream);
   if (err != hipSuccess) return err;
   const int tile = plan(gs, p.type, ws);

@@ -1,4 +1,5 @@
-// What the linear layer's kernels share (vn_linear.hip, vn_linear_wide.hip):
+// What the linear layer's kernels share (vn_linear.hip, vn_linear_wide.hip,
+// vn_linear_few.hip):
 // activations, the epilogue, the form of a product.
 #pragma once
 
@@ -248,5 +249,9 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t 
 // operands that wide_applies to; tiles of 256 x tn (256 or 128), no splits.
 bool wide_applies(const Product& g);
 hipError_t launch_wide(Product g, int tn, hipStream_t stream);
+
+// The product of few rows (vn_linear_few.hip): at most 32, both operands row-major.
+bool few_applies(const Product& g);
+hipError_t launch_few(const Product& g, Elem type, hipStream_t stream);
 
 }  // namespace vn

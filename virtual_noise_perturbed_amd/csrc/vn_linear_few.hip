@@ -1,0 +1,126 @@
+// The linear layer for few rows (gfx950), as serving calls it: y = act(x W^T + b) + r
+// with at most 16 MB rows.  What bounds it is reading W once, so every byte of W
+// goes from memory straight into the matrix cores' registers: a workgroup takes 16
+// rows of W (16 columns of y), its 8 waves a share of k each, with U loads of 16
+// bytes a lane on their way; x, which all workgroups read, comes from the L2.  The
+// waves' sums join in LDS, in wave order.
+//   bf16: v_mfma_f32_16x16x32_bf16; fp32: v_mfma_f32_16x16x4_f32 (whole fp32
+//   products; the matrix cores wait for W at any rate).
+#include "vn_linear.hpp"
+
+namespace vn {
+namespace {
+
+constexpr int WAVES = 8;
+
+// One 16-byte load of a lane: PER elements of a row; a step of k is 4 of them.
+template <typename T> struct Piece { static constexpr int PER = 16 / sizeof(T), STEP = 4 * PER; };
+
+__device__ __forceinline__ f32x4 multiply(const u32x4_any& w, const u32x4_any& x, f32x4 acc, const __bf16*) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply(const u32x4_any& w, const u32x4_any& x, f32x4 acc, const float*) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, static_cast<uint32_t>(w[i])),
+                                               __builtin_bit_cast(float, static_cast<uint32_t>(x[i])), acc, 0, 0, 0);
+  return acc;
+}
+
+// Elements [k, k + PER) of a row of n, zeros past its end.
+template <typename T>
+__device__ __forceinline__ u32x4_any load_ragged(const T* row, int64_t k, int64_t n) {
+  T e[Piece<T>::PER];
+#pragma unroll
+  for (int i = 0; i < Piece<T>::PER; ++i) e[i] = k + i < n ? row[k + i] : static_cast<T>(0.0f);
+  return __builtin_bit_cast(u32x4_any, e);
+}
+
+template <typename T, int MB>
+__global__ __launch_bounds__(64 * WAVES) void few_kernel(Product g) {
+  constexpr int PER = Piece<T>::PER, STEP = Piece<T>::STEP, U = 8 / MB;
+  __shared__ float sums[WAVES][MB * 16][20];   // (rows of 20: 16-byte writes spread over the banks)
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int r = lane & 15, part = lane >> 4;
+  // rows past the end are read from the last; they reach only outputs that are not stored
+  const T* w = static_cast<const T*>(g.b.p) + (n0 + r < g.n ? n0 + r : g.n - 1) * g.b.ld;
+  const T* x[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    const int64_t m = b * 16 + r;
+    x[b] = static_cast<const T*>(g.a.p) + (m < g.m ? m : g.m - 1) * g.a.ld;
+  }
+  // this wave's share of the steps, in one piece
+  const int64_t steps = (g.k + STEP - 1) / STEP, per = (steps + WAVES - 1) / WAVES;
+  const int64_t begin = wave * per * STEP;
+  const int64_t end = (wave + 1) * per * STEP < g.k ? (wave + 1) * per * STEP : g.k;
+  f32x4 acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = f32x4{};
+  int64_t k = begin + part * PER;
+  const int64_t whole = begin + (end - begin) / STEP * STEP + part * PER;
+  for (; k + (U - 1) * STEP < whole; k += U * STEP) {
+    u32x4_any fw[U], fx[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) __builtin_memcpy(&fw[u], w + k + u * STEP, 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) __builtin_memcpy(&fx[u][b], x[b] + k + u * STEP, 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < MB; ++b) acc[b] = multiply(fw[u], fx[u][b], acc[b], static_cast<const T*>(nullptr));
+  }
+  for (; k - part * PER < end; k += STEP) {
+    u32x4_any fw, fx[MB];
+    if (k < whole) {
+      __builtin_memcpy(&fw, w + k, 16);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) __builtin_memcpy(&fx[b], x[b] + k, 16);
+    } else {
+      fw = load_ragged(w, k, end);
+#pragma unroll
+      for (int b = 0; b < MB; ++b) fx[b] = load_ragged(x[b], k, end);
+    }
+#pragma unroll
+    for (int b = 0; b < MB; ++b) acc[b] = multiply(fw, fx[b], acc[b], static_cast<const T*>(nullptr));
+  }
+  // lane l holds row l % 16 of x at columns 4 (l / 16) .. + 3
+#pragma unroll
+  for (int b = 0; b < MB; ++b)
+    *reinterpret_cast<f32x4*>(&sums[wave][b * 16 + r][part * 4]) = acc[b];
+  __syncthreads();
+  const int m = threadIdx.x >> 1, c = (threadIdx.x & 1) * 8;
+  const int64_t n = n0 + c;
+  if (m >= g.m || m >= MB * 16 || n >= g.n) return;
+  float z[1][8] = {}, bias[8];
+  RawRun res[1];
+  load_bias(g.e, n, g.n, bias);
+  if (g.e.residual != nullptr) res[0] = load_raw<true>(g.e.residual, g.e.out_type, m, n, g.n);
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) z[0][j] += sums[i][m][c + j];
+  finish<1, true>(g.e, {m}, {true}, n, g.n, bias, res, z);
+}
+
+template <typename T>
+void launch_few_of(const Product& g, hipStream_t stream) {
+  const unsigned grid = static_cast<unsigned>((g.n + 15) / 16);
+  if (g.m <= 16) few_kernel<T, 1><<<grid, 64 * WAVES, 0, stream>>>(g);
+  else few_kernel<T, 2><<<grid, 64 * WAVES, 0, stream>>>(g);
+}
+
+}  // namespace
+
+bool few_applies(const Product& g) { return g.m <= 32 && !g.a.k_major && !g.b.k_major; }
+
+hipError_t launch_few(const Product& g, Elem type, hipStream_t stream) {
+  if (type == Elem::f32) launch_few_of<float>(g, stream);
+  else launch_few_of<__bf16>(g, stream);
+  return hipGetLastError();
+}
+
+}  // namespace vn
