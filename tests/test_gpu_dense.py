@@ -656,3 +656,32 @@ def test_linear_backward_wide(shape):
     within(db, dy.double().sum(0), (m + 4) * ref.U * az.sum(0) + 1e-30, "db")
     again = vn.linear_backward(dev(dy), dev(x), dev(w), weight_gradient_dtype=F32)
     assert all(torch.equal(a, b) for a, b in zip(again, (dx, dw, db)))
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")], ids=str)
+def test_layer_norm_larger_than_the_caches(types):
+    """Tensors that go past the caches: the first and the last rows against 64 bits, the column sums against fp32's."""
+    print("layer_norm large", types, flush=True)
+    gt, dt = TYPES[types[0]], TYPES[types[1]]
+    m, n = 40003, 2049
+    gen = torch.Generator(device=device()).manual_seed(m)
+    x, dy = (torch.randn(m, n, generator=gen, device=device()).to(t) for t in (dt, gt))
+    w, b = torch.randn(n, generator=gen, device=device()), torch.randn(n, generator=gen, device=device())
+    y, mean, rstd = vn.layer_norm(x, w, b, stats=True)
+    dx, dw, db = vn.layer_norm_backward(dy, x, mean, rstd, w)
+    cpu = lambda t, rows: t[rows].cpu()
+    for rows in (slice(0, 5), slice(m - 5, m)):
+        xr, wr, br = cpu(x, rows), w.cpu(), b.cpu()
+        want = ref.layer_norm(xr, wr, br, 1e-5)
+        within(cpu(y, rows), want[0], ref.layer_norm_bounds(xr, wr, br, *want, dt)[0], "y")
+        mr, rr, dr = cpu(mean, rows), cpu(rstd, rows), cpu(dy, rows)
+        want = ref.layer_norm_backward(dr, xr, mr, rr, wr)
+        within(cpu(dx, rows), want[0], ref.layer_norm_backward_bounds(dr, xr, mr, rr, wr, want[0], 5, dt)[0], "dx")
+    sums = [torch.zeros(n, dtype=torch.float64, device=device()) for _ in range(4)]
+    for i in range(0, m, 4096):
+        g, h = dy[i:i + 4096].double(), (x[i:i + 4096].double() - mean[i:i + 4096, None].double()) * rstd[i:i + 4096, None].double()
+        for s, t in zip(sums, ((g * h), g, (g * h).abs(), g.abs())):
+            s += t.sum(0)
+    sums = [s.cpu() for s in sums]
+    within(dw, sums[0], (m + 8) * ref.U * sums[2], "dweight")
+    within(db, sums[1], (m + 8) * ref.U * sums[3], "dbias")

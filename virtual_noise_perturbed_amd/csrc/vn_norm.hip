@@ -10,7 +10,7 @@
 // mean of a constant row is the constant.
 //
 // What bounds it: the bytes of x, dy, y and dx, each touched once.  A row of
-// up to 16384 (backward: 8192) is held in registers by G lanes, NV runs of 8 elements a lane;
+// up to 16384 is held in registers by G lanes, NV runs of 8 elements a lane;
 // the lanes keep their columns from row to row, so the weights are loaded once
 // per workgroup and a backward pass's column sums stay in registers until the
 // workgroup has walked all its rows (blockIdx.x, + gridDim.x, ...).  The next
@@ -23,7 +23,7 @@
 namespace vn {
 namespace {
 
-constexpr int64_t kMaxResident = 16384;   // longest row held in registers (forward; half of it backward)
+constexpr int64_t kMaxResident = 16384;   // longest row held in registers
 
 // Sum of v over the G lanes of a row; G > 64 spans waves of the workgroup and
 // goes through `red` (two slots of G / 64 values, alternated by the caller so
@@ -70,7 +70,7 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
 
 template <int G> constexpr int block_threads() { return G > 256 ? G : 256; }
 
-template <typename XT, typename YT, int G, int NV>
+template <typename XT, typename YT, int G, int NV, bool PAST>
 __global__ __launch_bounds__(block_threads<G>()) void norm_kernel(NormParams p) {
   constexpr int ROWS = block_threads<G>() / G;
   __shared__ float red[G > 64 ? 4 * (G / 64) : 1];
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_kernel(NormParams p) 
         run_values(cur[j], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * rstd * w[j][i] + b[j][i];
-        if (c < n) store_run(y + r * n, c, n, v);
+        if (c < n) store_run<PAST>(y + r * n, c, n, v);
       }
       if (lane == 0) {
         if (p.mean != nullptr) p.mean[r] = mean;
@@ -201,26 +201,38 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
 // Gradients.  Column sums of the rows a workgroup walked go to
 // partial[blockIdx.x][2][n] (dw, then db), added in workgroup order by
 // join_columns_kernel: the same bits on every call.
-template <typename GT, typename XT, int G, int NV>
+template <typename GT, typename XT, int G, int NV, bool PAST>
 __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormBackwardParams p) {
   constexpr int T = block_threads<G>();
   constexpr int ROWS = T / G;
+  // (4 runs a lane of fp32 rows leave no registers for a second row)
+  constexpr bool AHEAD = NV < 4 || (sizeof(GT) == 2 && sizeof(XT) == 2);
   __shared__ float red[G > 64 ? 4 * (G / 64) : 1];
+  // (nor for the column sums: those live in LDS, each lane's own, 16 bytes at a time)
+  constexpr bool IN_LDS = NV >= 4;
+  static_assert(!IN_LDS || ROWS == 1);
   __shared__ float join[ROWS > 1 ? T * NV * 8 : 1];
+  __shared__ float4 held[IN_LDS ? 4 * NV * T : 1];
   const int lane = threadIdx.x % G;
   const int n = static_cast<int>(p.n);
   const float count = static_cast<float>(n);
   const GT* __restrict__ dy = static_cast<const GT*>(p.dy);
   const XT* __restrict__ x = static_cast<const XT*>(p.x);
   XT* __restrict__ dx = static_cast<XT*>(p.dx);
-  float w[NV][8], sw[NV][8], sb[NV][8];
+  float w[NV][8], sw[IN_LDS ? 1 : NV][8], sb[IN_LDS ? 1 : NV][8];
+  // quarter q of run j's sums (dw: 0, 1; db: 2, 3)
+  auto slot = [&](int j, int q) -> float4& { return held[(j * 4 + q) * T + threadIdx.x]; };
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       w[j][i] = 1.0f;
-      sw[j][i] = 0.0f;
-      sb[j][i] = 0.0f;
+      sw[IN_LDS ? 0 : j][i] = 0.0f;
+      sb[IN_LDS ? 0 : j][i] = 0.0f;
+    }
+    if constexpr (IN_LDS) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) slot(j, q) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     if (p.weight != nullptr) run_values(load_run(p.weight, (j * G + lane) * 8, n), w[j]);
   }
@@ -236,15 +248,16 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * G + lane) * 8;
-      nx[j] = load_run(x + q * n, c, n);
-      ng[j] = load_run(dy + q * n, c, n);
+      nx[j] = load_run<PAST>(x + q * n, c, n);
+      ng[j] = load_run<PAST>(dy + q * n, c, n);
     }
     nmean = p.mean[q];
     nrstd = p.rstd[q];
   };
-  if (r0 < p.rows) fetch(r);
+  if (AHEAD && r0 < p.rows) fetch(r);
   int par = 0;
   for (int64_t base = r0; base < p.rows; base += step, r += step) {
+    if (!AHEAD) fetch(r);
     Run8<XT> cx[NV];
     Run8<GT> cg[NV];
     const float mean = nmean, rstd = nrstd;
@@ -253,7 +266,7 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
       cx[j] = nx[j];
       cg[j] = ng[j];
     }
-    if (base + step < p.rows) fetch(r + step);
+    if (AHEAD && base + step < p.rows) fetch(r + step);
     const bool valid = r < p.rows;
     float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -262,18 +275,32 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
       float xv[8], gv[8];
       run_values(cx[j], xv);
       run_values(cg[j], gv);
+      float tv[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // (columns past n hold dy = 0; their x - mean is not formed, so that an
         // infinite statistic there cannot turn a zero into NaN)
         const float h = c + i < n ? (xv[i] - mean) * rstd : 0.0f;
         const float t = gv[i] * h, g = gv[i] * w[j][i];
-        if (valid) {
+        tv[i] = t;
+        if (!IN_LDS && valid) {
           sw[j][i] += t;
           sb[j][i] += gv[i];
         }
         a += g;
         b += g * h;
+      }
+      if constexpr (IN_LDS) {   // (one row a workgroup: every row is valid)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float* v = (q < 2 ? tv : gv) + (q & 1) * 4;
+          float4 t = slot(j, q);
+          t.x += v[0];
+          t.y += v[1];
+          t.z += v[2];
+          t.w += v[3];
+          slot(j, q) = t;
+        }
       }
     }
     row_sum2<G>(a, b, red + (G > 64 ? par * 2 * (G / 64) : 0));
@@ -289,13 +316,13 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
         run_values(cg[j], gv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) xv[i] = rstd * (gv[i] * w[j][i] - a - (xv[i] - mean) * rstd * b);
-        if (c < n) store_run(dx + r * n, c, n, xv);
+        if (c < n) store_run<PAST>(dx + r * n, c, n, xv);
       }
     }
   }
   if (p.dweight == nullptr && p.dbias == nullptr) return;
   // Several rows side by side: their sums join in row order.
-  auto join_rows = [&](float (&s)[NV][8]) {
+  auto join_rows = [&](float (&s)[IN_LDS ? 1 : NV][8]) {
     if constexpr (ROWS > 1) {
       __syncthreads();
 #pragma unroll
@@ -309,22 +336,36 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float t = 0.0f;
+#pragma unroll 4
             for (int k = 0; k < ROWS; ++k) t += join[(j * 8 + i) * T + k * G + threadIdx.x];
             s[j][i] = t;
           }
       }
     }
   };
-  join_rows(sw);
-  join_rows(sb);
+  if constexpr (!IN_LDS) {
+    join_rows(sw);
+    join_rows(sb);
+  }
   if (threadIdx.x < G) {
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * n;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * G + lane) * 8;
       if (c < n) {
-        store_run(out, c, n, sw[j]);
-        store_run(out + n, c, n, sb[j]);
+        if constexpr (IN_LDS) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 t = slot(j, q);
+            float* v = (q < 2 ? sw : sb)[0] + (q & 1) * 4;
+            v[0] = t.x;
+            v[1] = t.y;
+            v[2] = t.z;
+            v[3] = t.w;
+          }
+        }
+        store_run(out, c, n, sw[IN_LDS ? 0 : j]);
+        store_run(out + n, c, n, sb[IN_LDS ? 0 : j]);
       }
     }
   }
@@ -400,26 +441,40 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBackwardParams p) 
   store_run(out + n, c, n, sb);
 }
 
-// Sums of partial rows in a fixed order: 64 columns by 4 waves, each a quarter
-// of the rows, joined in wave order.  Blocks of grid.y 1 take the second sum,
-// n further on in each partial row.
-__global__ __launch_bounds__(256) void join_columns_kernel(const float* partial, int64_t parts, int64_t pitch,
-                                                           int64_t n, float* first, float* second) {
-  __shared__ float s[256];
+// Sums of partial rows in a fixed order: 64 columns by 16 waves, each a
+// sixteenth of the rows with 8 loads on their way, joined in wave order (4 waves
+// with a load at a time took 32 us for 512 rows of any width; these take 5).
+// Blocks of grid.y 1 take the second sum, n further on in each partial row.
+__global__ __launch_bounds__(1024) void join_columns_kernel(const float* partial, int64_t parts, int64_t pitch,
+                                                            int64_t n, float* first, float* second) {
+  __shared__ float s[1024];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + lane;
   float* out = blockIdx.y == 0 ? first : second;
   if (out == nullptr) return;
   float t = 0.0f;
   if (c < n) {
-    const int64_t per = (parts + 3) / 4;
+    const int64_t per = (parts + 15) / 16;
     const int64_t end = (wave + 1) * per < parts ? (wave + 1) * per : parts;
     const float* src = partial + blockIdx.y * n + c;
-    for (int64_t k = wave * per; k < end; ++k) t += src[k * pitch];
+    int64_t k = wave * per;
+    for (; k + 8 <= end; k += 8) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = src[(k + i) * pitch];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t += v[i];
+    }
+    for (; k < end; ++k) t += src[k * pitch];
   }
   s[threadIdx.x] = t;
   __syncthreads();
-  if (wave == 0 && c < n) out[c] = ((s[lane] + s[lane + 64]) + s[lane + 128]) + s[lane + 192];
+  if (wave == 0 && c < n) {
+    t = s[lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) t += s[w * 64 + lane];
+    out[c] = t;
+  }
 }
 
 // The layout of a row over lanes: G lanes of NV runs each.
@@ -427,14 +482,16 @@ struct RowShape {
   int g, nv;
 };
 RowShape row_shape(int64_t n, bool backward) {
+  if (n <= 64) return {8, 1};
   if (n <= 128) return {16, 1};
+  if (n <= 256) return {32, 1};
   if (n <= 512) return {64, 1};
   if (n <= 1024) return {64, 2};
   if (n <= 2048) return {256, 1};
   if (n <= 4096) return {256, 2};
   if (n <= 8192) return {512, 2};
-  // (a backward lane also holds the column sums and two rows: 16 waves have no registers for that)
-  if (n <= kMaxResident && !backward) return {1024, 2};
+  // (a backward lane holds the column sums too: 16 waves have no registers for that)
+  if (n <= kMaxResident) return backward ? RowShape{512, 4} : RowShape{1024, 2};
   return {0, 0};
 }
 
@@ -443,13 +500,17 @@ template <bool BACKWARD, typename F>
 hipError_t with_shape(RowShape s, F&& f) {
 #define VN_SHAPE(G_, NV_) \
   if (s.g == G_ && s.nv == NV_) return f(std::integral_constant<int, G_>{}, std::integral_constant<int, NV_>{});
+  VN_SHAPE(8, 1)
   VN_SHAPE(16, 1)
+  VN_SHAPE(32, 1)
   VN_SHAPE(64, 1)
   VN_SHAPE(64, 2)
   VN_SHAPE(256, 1)
   VN_SHAPE(256, 2)
   VN_SHAPE(512, 2)
-  if constexpr (!BACKWARD) {
+  if constexpr (BACKWARD) {
+    VN_SHAPE(512, 4)
+  } else {
     VN_SHAPE(1024, 2)
   }
 #undef VN_SHAPE
@@ -463,19 +524,30 @@ hipError_t with_types(Elem a, Elem b, F&& f) {
 }
 
 constexpr int64_t kNormGrid = 2048;       // workgroups of 256: 8 per CU
-constexpr int64_t kBackwardGrid = 512;    // 2 per CU: their partial sums are written and read once more
+// Workgroups of a backward pass, whose partial sums are written and read once more:
+// 2 per CU, 4 for short rows (30000 x 257 fp32: 35 us on 512, 27 on
+// 1024; 5003 x 1001: 20 and 24).
+int64_t backward_grid(int64_t n) { return n <= 512 ? 1024 : 512; }
 
 int64_t backward_parts(int64_t rows, int64_t n) {
   const RowShape s = row_shape(n, true);
   if (s.g == 0) return rows < 64 ? rows : 64;
   const int64_t per = s.g > 256 ? 1 : 256 / s.g;
   const int64_t blocks = (rows + per - 1) / per;
-  return blocks < kBackwardGrid ? blocks : kBackwardGrid;
+  return blocks < backward_grid(n) ? blocks : backward_grid(n);
 }
+
+// Tensors of more bytes than this go past the caches (256 MiB): at 32768 x 4096 in
+// bf16 the forward's stores then take it from 107 to 103 us (5.2 TB/s), the
+// backward's loads and stores from 152 to 143 (5.6 TB/s); 2000 x 1024, which the
+// caches hold, would go from 4.8 to 6.7 us.
+constexpr int64_t kCaches = int64_t{256} << 20;
+int64_t bytes_of(Elem t) { return t == Elem::f32 ? 4 : 2; }
 
 }  // namespace
 
 hipError_t launch_layer_norm(const NormParams& p, hipStream_t stream) {
+  const bool past = p.rows * p.n * (bytes_of(p.x_type) + bytes_of(p.y_type)) > kCaches;
   const RowShape s = row_shape(p.n, false);
   return with_types(p.x_type, p.y_type, [&](auto xt, auto yt) -> hipError_t {
     using XT = decltype(xt);
@@ -489,8 +561,9 @@ hipError_t launch_layer_norm(const NormParams& p, hipStream_t stream) {
       const int64_t per = T / g.value;
       const int64_t blocks = (p.rows + per - 1) / per;
       const int64_t most = kNormGrid * 256 / T;
-      norm_kernel<XT, YT, decltype(g)::value, decltype(nv)::value>
-          <<<static_cast<unsigned>(blocks < most ? blocks : most), T, 0, stream>>>(p);
+      const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
+      if (past) norm_kernel<XT, YT, decltype(g)::value, decltype(nv)::value, true><<<grid, T, 0, stream>>>(p);
+      else norm_kernel<XT, YT, decltype(g)::value, decltype(nv)::value, false><<<grid, T, 0, stream>>>(p);
       return hipGetLastError();
     });
   });
@@ -501,6 +574,7 @@ int64_t layer_norm_backward_workspace(int64_t rows, int64_t n) {
 }
 
 hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t stream) {
+  const bool past = p.rows * p.n * (bytes_of(p.dy_type) + 2 * bytes_of(p.x_type)) > kCaches;
   const RowShape s = row_shape(p.n, true);
   const int64_t parts = backward_parts(p.rows, p.n);
   const bool sums = p.dweight != nullptr || p.dbias != nullptr;
@@ -518,8 +592,10 @@ hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t s
         return hipGetLastError();
       }
       return with_shape<true>(s, [&](auto g, auto nv) -> hipError_t {
-        norm_backward_kernel<GT, XT, decltype(g)::value, decltype(nv)::value>
-            <<<static_cast<unsigned>(parts), block_threads<decltype(g)::value>(), 0, stream>>>(p);
+        constexpr int T = block_threads<decltype(g)::value>();
+        const unsigned grid = static_cast<unsigned>(parts);
+        if (past) norm_backward_kernel<GT, XT, decltype(g)::value, decltype(nv)::value, true><<<grid, T, 0, stream>>>(p);
+        else norm_backward_kernel<GT, XT, decltype(g)::value, decltype(nv)::value, false><<<grid, T, 0, stream>>>(p);
         return hipGetLastError();
       });
     });
@@ -530,7 +606,7 @@ hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t s
 
 hipError_t launch_join_columns(const float* partial, int64_t parts, int64_t pitch, int64_t n, float* first,
                                float* second, hipStream_t stream) {
-  join_columns_kernel<<<dim3(static_cast<unsigned>((n + 63) / 64), second != nullptr ? 2 : 1), 256, 0, stream>>>(
+  join_columns_kernel<<<dim3(static_cast<unsigned>((n + 63) / 64), second != nullptr ? 2 : 1), 1024, 0, stream>>>(
       partial, parts, pitch, n, first, second);
   return hipGetLastError();
 }

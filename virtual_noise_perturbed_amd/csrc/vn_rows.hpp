@@ -84,6 +84,35 @@ __device__ __forceinline__ void store_run(T* row, I c, I n, const float (&v)[8])
   }
 }
 
+// The same past the caches (PAST; runs that are whole): for tensors that the
+// caches cannot hold until they are read again.
+template <bool PAST, typename T, typename I>
+__device__ __forceinline__ void store_run(T* row, I c, I n, const float (&v)[8]) {
+  if (PAST && c + 8 <= n) {
+    const Run8<T> r = make_run(v, row);
+    u32x4_any part[sizeof(r) / 16];
+    __builtin_memcpy(part, &r, sizeof(r));
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(r) / 16; ++i)
+      __builtin_nontemporal_store(part[i], reinterpret_cast<u32x4_any*>(row + c) + i);
+  } else {
+    store_run(row, c, n, v);
+  }
+}
+template <bool PAST, typename T, typename I>
+__device__ __forceinline__ Run8<T> load_run(const T* row, I c, I n) {
+  if (PAST && c + 8 <= n) {
+    Run8<T> r;
+    u32x4_any part[sizeof(r) / 16];
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(r) / 16; ++i)
+      part[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(row + c) + i);
+    __builtin_memcpy(&r, part, sizeof(r));
+    return r;
+  }
+  return load_run(row, c, n);
+}
+
 // Sum over the aligned group of G lanes that holds this lane (G a power of
 // two, at most 64), in every lane of the group, in a fixed order.
 template <int G>

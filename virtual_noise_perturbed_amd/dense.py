@@ -203,7 +203,10 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     w, b = _vector("weight", weight, n, dev), _vector("bias", bias, n, dev)
     out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
     out_kind = _elem("out", out_dtype)
-    y = _output("out", out, x.shape, out_dtype, dev)
+    if out is None and out_dtype == x.dtype and x.is_contiguous():
+        y = torch.empty_like(x)
+    else:
+        y = _output("out", out, x.shape, out_dtype, dev)
     mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev) if stats else None
     rstd = torch.empty_like(mean) if stats else None
     xc = x if x.is_contiguous() else x.contiguous()
