@@ -139,10 +139,11 @@ def test_layer_norm_backward_validation(lib):
     for name in ("dy", "x", "w", "mean", "rstd", "dx", "dw", "db", "ws"):
         assert norm_backward(lib, **{name: ODD}) == E.VN_ERR_ALIGN
     f = lib.vn_layer_norm_backward_workspace_size
-    st, need = size_of(f, 3, 8)
+    st, need = size_of(f, 3000, 8)
     assert st == E.VN_OK and need > 0
-    assert norm_backward(lib, wsb=need - 1) == E.VN_ERR_SHAPE
-    assert norm_backward(lib, ws=None, wsb=need) == E.VN_ERR_NULL
+    assert norm_backward(lib, rows=3000, wsb=need - 1) == E.VN_ERR_SHAPE
+    assert norm_backward(lib, rows=3000, ws=None, wsb=need) == E.VN_ERR_NULL
+    assert size_of(f, 3, 8) == (E.VN_OK, 0)   # (one workgroup: no partial sums)
     assert f(3, 8, None) == E.VN_ERR_NULL
     assert size_of(f, -1, 8)[0] == E.VN_ERR_SHAPE
     assert norm_backward(lib, rows=0, n=0, dy=None, x=None) == E.VN_OK

@@ -27,15 +27,11 @@ __device__ __forceinline__ void static_for(F&& f) {
 }
 
 // ---- activations -----------------------------------------------------------
-// The hardware's exponential and reciprocal (a unit of the last place each); the
-// rounding of x log2(e) is put right, so that large arguments keep that accuracy.
+// The hardware's exponential and reciprocal (a unit of the last place each).  The
+// rounded x log2(e) costs the exponential |x| units, where it is that far from 1:
+// in the tails, which end up below a unit of z.
 
-__device__ __forceinline__ float exp_of(float x) {
-  x = __builtin_amdgcn_fmed3f(x, -150.0f, 150.0f);   // 0 and infinity past fp32's range
-  const float t = x * 1.44269504088896341f;
-  const float rest = __builtin_fmaf(x, 1.44269504088896341f, -t) + x * 1.92596299e-8f;
-  return __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.69314718055994531f, 1.0f);
-}
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 __device__ __forceinline__ float sigmoid_of(float x) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-x)); }
 
 // The normal distribution's integral up to z, within 1.0e-7, and e = exp(-z^2 / 2):
@@ -48,7 +44,7 @@ __device__ __forceinline__ float normal_of(float z, float& e) {
   p = __builtin_fmaf(t, p, 0.5f * 1.421413741f);
   p = __builtin_fmaf(t, p, 0.5f * -0.284496736f);
   p = __builtin_fmaf(t, p, 0.5f * 0.254829592f);
-  e = exp_of(-0.5f * z * z);
+  e = __builtin_amdgcn_exp2f(z * z * (-0.5f * 1.44269504088896341f));
   const float tail = t * p * e;
   return z > 0.0f ? 1.0f - tail : tail;
 }

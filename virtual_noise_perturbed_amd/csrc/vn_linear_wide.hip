@@ -253,14 +253,16 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(Product g) {
 
   // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
   // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS
-  // of its own, to leave in runs of 8: two per lane and turn, one copy of the code
+  // of its own, to leave in runs of 8: four per lane and turn, one copy of the code
   // for all turns (unrolled, the epilogue was bound by the instruction cache's
-  // misses), the residual loaded three turns ahead.
+  // misses), the residual loaded a turn ahead.
   __syncthreads();
   float* out = reinterpret_cast<float*>(smem) + wave * 32 * OUT_PITCH;
   const int l32 = lane & 31, lh = lane >> 5;
   constexpr int LANES = WN / 8, ROWS = 64 / LANES;   // lanes of a row, rows at a time
-  constexpr int TURNS = 32 / ROWS / 2;               // of a block
+  constexpr int RUNS = 4;                            // a lane and turn
+  constexpr int TURNS = 32 / ROWS / RUNS;            // of a block
+  constexpr int AHEAD = 1;                           // turns that the residual is loaded ahead
   const Epilogue e = g.e;
   const int64_t col = n0 + wn * WN + lane % LANES * 8;
   const int64_t row0 = m0 + wm * 128 + lane / LANES;
@@ -268,16 +270,16 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(Product g) {
   load_bias(e, col, g.n, bias);
   auto epilogue = [&](auto checked_c) {
     constexpr bool CHECKED = decltype(checked_c)::value;
-    RawRun ahead[3][2];
-    auto fetch = [&](int p, RawRun (&r)[2]) {
+    RawRun ahead[AHEAD][RUNS];
+    auto fetch = [&](int p, RawRun (&r)[RUNS]) {
       if (e.residual == nullptr || p >= 4 * TURNS) return;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int64_t row = row0 + (2 * p + i) * ROWS;
+      for (int i = 0; i < RUNS; ++i) {
+        const int64_t row = row0 + (RUNS * p + i) * ROWS;
         if (!CHECKED || (row < g.m && col < g.n)) r[i] = load_raw<CHECKED>(e.residual, e.out_type, row, col, g.n);
       }
     };
-    static_for<3>([&](auto p) { fetch(decltype(p)::value, ahead[decltype(p)::value]); });
+    static_for<AHEAD>([&](auto p) { fetch(decltype(p)::value, ahead[decltype(p)::value]); });
 #pragma unroll 1
     for (int p = 0; p < 4 * TURNS; ++p) {
       if (p % TURNS == 0) {
@@ -297,22 +299,22 @@ __global__ __launch_bounds__(256, 1) void wide_kernel(Product g) {
         });
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
-      float z[2][8];
-      int64_t row[2];
-      bool ok[2];
-      RawRun res[2];
+      float z[RUNS][8];
+      int64_t row[RUNS];
+      bool ok[RUNS];
+      RawRun res[RUNS];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        row[i] = row0 + (2 * p + i) * ROWS;
+      for (int i = 0; i < RUNS; ++i) {
+        row[i] = row0 + (RUNS * p + i) * ROWS;
         ok[i] = row[i] < g.m && col < g.n;
         res[i] = ahead[0][i];
-        ahead[0][i] = ahead[1][i];
-        ahead[1][i] = ahead[2][i];
-        const int r = (2 * (p % TURNS) + i) * ROWS + lane / LANES;
+#pragma unroll
+        for (int a = 0; a + 1 < AHEAD; ++a) ahead[a][i] = ahead[a + 1][i];
+        const int r = (RUNS * (p % TURNS) + i) * ROWS + lane / LANES;
         __builtin_memcpy(z[i], __builtin_assume_aligned(out + r * OUT_PITCH + lane % LANES * 8, 16), 32);
       }
-      fetch(p + 3, ahead[2]);
-      finish<2, CHECKED>(e, row, ok, col, g.n, bias, res, z);
+      fetch(p + AHEAD, ahead[AHEAD - 1]);
+      finish<RUNS, CHECKED>(e, row, ok, col, g.n, bias, res, z);
     }
   };
   if (m0 + TM <= g.m && n0 + TN <= g.n) epilogue(std::false_type{});

@@ -198,9 +198,19 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(NormParams p) {
   }
 }
 
-// Gradients.  Column sums of the rows a workgroup walked go to
-// partial[blockIdx.x][2][n] (dw, then db), added in workgroup order by
-// join_columns_kernel: the same bits on every call.
+// Where the column sums of part `i` of `parts` go: partial[i][2][n] (dw, then db),
+// or, with one part, to the gradients themselves.
+struct SumRows {
+  float* dw;
+  float* db;
+};
+__device__ __forceinline__ SumRows sum_rows(const NormBackwardParams& p, int64_t i, int64_t parts) {
+  if (parts == 1) return {p.dweight, p.dbias};
+  return {p.partial + i * 2 * p.n, p.partial + i * 2 * p.n + p.n};
+}
+
+// Gradients.  Column sums of the rows a workgroup walked are added in workgroup
+// order by join_columns_kernel: the same bits on every call.
 template <typename GT, typename XT, int G, int NV, bool PAST>
 __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormBackwardParams p) {
   constexpr int T = block_threads<G>();
@@ -348,7 +358,7 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
     join_rows(sb);
   }
   if (threadIdx.x < G) {
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * n;
+    const SumRows out = sum_rows(p, blockIdx.x, gridDim.x);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * G + lane) * 8;
@@ -364,8 +374,8 @@ __global__ __launch_bounds__(block_threads<G>()) void norm_backward_kernel(NormB
             v[3] = t.w;
           }
         }
-        store_run(out, c, n, sw[IN_LDS ? 0 : j]);
-        store_run(out + n, c, n, sb[IN_LDS ? 0 : j]);
+        if (out.dw != nullptr) store_run(out.dw, c, n, sw[IN_LDS ? 0 : j]);
+        if (out.db != nullptr) store_run(out.db, c, n, sb[IN_LDS ? 0 : j]);
       }
     }
   }
@@ -436,9 +446,9 @@ __global__ __launch_bounds__(256) void column_sums_kernel(NormBackwardParams p) 
       sb[i] += gv[i];
     }
   }
-  float* out = p.partial + static_cast<int64_t>(blockIdx.y) * 2 * n;
-  store_run(out, c, n, sw);
-  store_run(out + n, c, n, sb);
+  const SumRows out = sum_rows(p, blockIdx.y, gridDim.y);
+  if (out.dw != nullptr) store_run(out.dw, c, n, sw);
+  if (out.db != nullptr) store_run(out.db, c, n, sb);
 }
 
 // Sums of partial rows in a fixed order: 64 columns by 16 waves, each a
@@ -533,6 +543,8 @@ int64_t backward_parts(int64_t rows, int64_t n) {
   const RowShape s = row_shape(n, true);
   if (s.g == 0) return rows < 64 ? rows : 64;
   const int64_t per = s.g > 256 ? 1 : 256 / s.g;
+  // a few turns of one workgroup cost less than a second launch that joins the parts
+  if (rows <= 4 * per) return rows < 1 ? 0 : 1;
   const int64_t blocks = (rows + per - 1) / per;
   return blocks < backward_grid(n) ? blocks : backward_grid(n);
 }
@@ -570,7 +582,8 @@ hipError_t launch_layer_norm(const NormParams& p, hipStream_t stream) {
 }
 
 int64_t layer_norm_backward_workspace(int64_t rows, int64_t n) {
-  return backward_parts(rows, n) * 2 * n * static_cast<int64_t>(sizeof(float));
+  const int64_t parts = backward_parts(rows, n);
+  return parts > 1 ? parts * 2 * n * static_cast<int64_t>(sizeof(float)) : 0;
 }
 
 hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t stream) {
@@ -601,7 +614,7 @@ hipError_t launch_layer_norm_backward(const NormBackwardParams& p, hipStream_t s
     });
     if (e != hipSuccess) return e;
   }
-  return sums ? launch_join_columns(p.partial, parts, 2 * p.n, p.n, p.dweight, p.dbias, stream) : hipSuccess;
+  return sums && parts != 1 ? launch_join_columns(p.partial, parts, 2 * p.n, p.n, p.dweight, p.dbias, stream) : hipSuccess;
 }
 
 hipError_t launch_join_columns(const float* partial, int64_t parts, int64_t pitch, int64_t n, float* first,

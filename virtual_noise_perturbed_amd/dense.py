@@ -81,20 +81,30 @@ def _workspace_size(name: str, *sizes: int) -> int:
     return need.value
 
 
+def _replaced(shape: torch.Size, last: int):
+    return (shape[0], last) if len(shape) == 2 else shape[:-1] + (last,)
+
+
 def _rows(shape: torch.Size) -> int:
     return shape[0] if len(shape) == 2 else math.prod(shape[:-1])
 
 
 def _linear_operands(x: torch.Tensor, weight: torch.Tensor):
+    """Checks of the layer's operands: (element type, rows, in, out, device)."""
     _require_device("weight", weight)
-    _require_device("x", x, weight.device)
-    if weight.dim() != 2:
+    device, dtype = weight.device, weight.dtype
+    _require_device("x", x, device)
+    shape = weight.shape
+    if len(shape) != 2:
         raise ValueError("weight must be (out_features, in_features)")
-    if x.dtype != weight.dtype:
-        raise TypeError(f"x ({x.dtype}) and weight ({weight.dtype}) must share a dtype")
-    if x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+    if x.dtype != dtype:
+        raise TypeError(f"x ({x.dtype}) and weight ({dtype}) must share a dtype")
+    out_f, in_f = shape
+    xs = x.shape
+    if not xs or xs[-1] != in_f:
         raise ValueError("x and weight disagree on in_features")
-    return _elem("weight", weight.dtype), _rows(x.shape)
+    kind = _ELEM.get(dtype)
+    return (_elem("weight", dtype) if kind is None else kind), _rows(xs), in_f, out_f, device
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -111,15 +121,17 @@ def linear(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] =
     ``x @ weight^T + bias``, for ``linear_backward``.
     """
     lib = _lib.load()
-    kind, rows = _linear_operands(x, weight)
-    dev = weight.device
-    out_f, in_f = weight.shape
-    shape = x.shape[:-1] + (out_f,)
+    kind, rows, in_f, out_f, dev = _linear_operands(x, weight)
+    shape = _replaced(x.shape, out_f)
     act = _activation(activation)
     b = _vector("bias", bias, out_f, dev)
-    out_dtype = (x.dtype if out is None else out.dtype) if out_dtype is None else out_dtype
-    out_kind = _elem("out", out_dtype)
-    y = _output("out", out, shape, out_dtype, dev)
+    if out is None and out_dtype is None:
+        out_dtype, out_kind = x.dtype, kind
+        y = x.new_empty(shape)
+    else:
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+        out_kind = _elem("out", out_dtype)
+        y = _output("out", out, shape, out_dtype, dev)
     if pre is not None:
         _output("pre", pre, shape, x.dtype, dev)
     r = None
@@ -151,10 +163,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
     ``dy * act'(pre)`` is rounded to bfloat16 for dx and dweight.
     """
     lib = _lib.load()
-    kind, rows = _linear_operands(x, weight)
-    dev = weight.device
-    out_f, in_f = weight.shape
-    shape = x.shape[:-1] + (out_f,)
+    kind, rows, in_f, out_f, dev = _linear_operands(x, weight)
+    shape = _replaced(x.shape, out_f)
     act = _activation(activation)
     _require_device("dy", dy, dev)
     if dy.shape != shape:
@@ -171,8 +181,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, act
     dw_dtype = weight.dtype if weight_gradient_dtype is None else weight_gradient_dtype
     dw_kind = _elem("weight_gradient_dtype", dw_dtype)
     dyc, xc, wc = _aligned(dy), _aligned(x), _aligned(weight)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
-    dw = torch.empty(weight.shape, dtype=dw_dtype, device=dev) if weight_gradient else None
+    dx = xc.new_empty(xc.shape) if input_gradient else None
+    dw = wc.new_empty(wc.shape, dtype=dw_dtype) if weight_gradient else None
     db = torch.empty((out_f,), dtype=torch.float32, device=dev) if bias_gradient else None
     wanted = (1 if input_gradient else 0) | (2 if weight_gradient else 0) | (4 if bias_gradient else 0)
     need = _workspace_size("vn_linear_backward", kind, dy_kind, rows, in_f, out_f, act, wanted)
@@ -243,12 +253,12 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
         if t.shape != x.shape[:-1] or t.dtype != torch.float32:
             raise ValueError(f"{name} must be {tuple(x.shape[:-1])} in float32")
     w = _vector("weight", weight, n, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if input_gradient else None
+    dyc, xc, mc, rc = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
+    dx = xc.new_empty(xc.shape) if input_gradient else None
     dw = torch.empty((n,), dtype=torch.float32, device=dev) if parameter_gradients else None
     db = torch.empty_like(dw) if parameter_gradients else None
     need = _workspace_size("vn_layer_norm_backward", rows, n) if parameter_gradients else 0
     ws = _workspace(need, dev)
-    dyc, xc, mc, rc = dy.contiguous(), x.contiguous(), mean.contiguous(), rstd.contiguous()
     st = lib.vn_layer_norm_backward(dyc.data_ptr(), dy_kind, xc.data_ptr(), kind, _ptr(w), mc.data_ptr(),
                                     rc.data_ptr(), rows, n, _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), need, _stream(dev))
     if st:
