@@ -1,0 +1,162 @@
+"""Trains the centre of a population on one GPU with the dense operators and the
+virtual-noise estimator together.
+
+A pre-norm residual network regresses a smooth function.  Its blocks are trained
+by their gradients (layer norm, linear layers with fused activation and residual,
+their backward passes, AdamW with 8-bit states on fp32 parameters whose bf16 copies the
+layers read).  Its head then follows a change of the target by evolution strategies: a
+population of virtual-noise perturbations of the head is evaluated in one call, the
+estimated gradient goes to a second AdamW, which ascends.
+
+    python examples/centre_training.py [--steps 200] [--width 256] [--blocks 2]
+"""
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import virtual_noise_perturbed_amd as vn  # noqa: E402
+
+BF16 = torch.bfloat16
+
+
+class Centre:
+    """in -> width, ``blocks`` of h + W2 gelu(W1 norm(h)), norm, width -> out."""
+
+    def __init__(self, n_in, width, blocks, n_out, device, seed=0, lr=3e-3):
+        gen = torch.Generator().manual_seed(seed)
+        self.blocks = blocks
+        self.params, self.copies, self.decay = [], [], []
+
+        def add(shape, scale=None, value=0.0):
+            """A parameter; matrices get a bf16 copy that the layers read."""
+            p = (torch.randn(shape, generator=gen) * scale if scale else torch.full(shape, value)).to(device)
+            self.params.append(p)
+            self.copies.append(p.to(BF16) if scale else None)
+            self.decay.append(0.01 if scale else 0.0)
+
+        add((width, n_in), n_in ** -0.5)
+        add((width,))
+        for _ in range(blocks):
+            add((width,), value=1.0)
+            add((width,))
+            add((width, width), width ** -0.5)
+            add((width,))
+            add((width, width), width ** -0.5)
+            add((width,))
+        add((width,), value=1.0)
+        add((width,))
+        add((n_out, width), width ** -0.5)
+        add((n_out,))
+        self.grads = [torch.zeros_like(p, dtype=p.dtype if c is None else BF16) for p, c in zip(self.params, self.copies)]
+        self.opt = vn.AdamW(self.params, self.grads, lr=lr, weight_decay=self.decay, copies=self.copies, state_bits=8,
+                            device_step=True)
+
+    def weight(self, i):
+        return self.params[i] if self.copies[i] is None else self.copies[i]
+
+    def features(self, x, keep=None):
+        """The head's input, bf16; ``keep`` receives what the backward pass needs."""
+        h = vn.linear(x, self.weight(0), self.weight(1))
+        for b in range(self.blocks):
+            at = 2 + 6 * b
+            n, mean, rstd = vn.layer_norm(h, self.weight(at), self.weight(at + 1), stats=True)
+            pre = torch.empty_like(h) if keep is not None else None
+            a = vn.linear(n, self.weight(at + 2), self.weight(at + 3), activation="gelu", pre=pre)
+            if keep is not None:
+                keep.append((h, mean, rstd, n, pre, a))
+            h = vn.linear(a, self.weight(at + 4), self.weight(at + 5), residual=h)
+        at = 2 + 6 * self.blocks
+        f, mean, rstd = vn.layer_norm(h, self.weight(at), self.weight(at + 1), stats=True)
+        if keep is not None:
+            keep.append((h, mean, rstd, f))
+        return f
+
+    def step(self, x, target):
+        """One training step; returns the loss before it (a tensor)."""
+        keep = []
+        f = self.features(x, keep)
+        at = 2 + 6 * self.blocks
+        y = vn.linear(f, self.weight(at + 2), self.weight(at + 3), out_dtype=torch.float32)
+        error = y - target
+        dy = error * (2.0 / error.numel())
+        grads = [None] * len(self.params)
+        df, grads[at + 2], grads[at + 3] = vn.linear_backward(dy, f, self.weight(at + 2))
+        h, mean, rstd, _ = keep.pop()
+        dh, grads[at], grads[at + 1] = vn.layer_norm_backward(df, h, mean, rstd, self.weight(at))
+        for b in reversed(range(self.blocks)):
+            at = 2 + 6 * b
+            h, mean, rstd, n, pre, a = keep.pop()
+            da, grads[at + 4], grads[at + 5] = vn.linear_backward(dh, a, self.weight(at + 4))
+            dn, grads[at + 2], grads[at + 3] = vn.linear_backward(da, n, self.weight(at + 2), activation="gelu", pre=pre)
+            through, grads[at], grads[at + 1] = vn.layer_norm_backward(dn, h, mean, rstd, self.weight(at))
+            dh = dh + through
+        _, grads[0], grads[1] = vn.linear_backward(dh, x, self.weight(0), input_gradient=False)
+        for have, new in zip(self.grads, grads):
+            have.copy_(new)
+        self.opt.step()
+        return error.square().mean()
+
+
+def tune_head(centre, x, target, steps, pop=128, sigma=0.02, lr=2e-3):
+    """Evolution strategies on the head: fitness is minus the loss; returns the centre's losses."""
+    device = x.device
+    at = 2 + 6 * centre.blocks
+    w, b = centre.params[at + 2], centre.params[at + 3]
+    f = centre.features(x).float()
+    n_out, width = w.shape
+    offsets = vn.compute_offsets([(n_out, width), (n_out,)])
+    grads = [torch.zeros_like(w), torch.zeros_like(b)]
+    opt = vn.AdamW([w, b], grads, lr=lr, weight_decay=0.0, maximize=True)
+    losses = []
+    for t in range(steps):
+        seeds = torch.arange(t * pop, (t + 1) * pop, device=device)
+        y = vn.virtual_perturbed_linear(f, w, b, seeds, sigma, offsets[0])
+        fitness = -(y - target).square().mean((1, 2))
+        fitness = (fitness - fitness.mean()) / (fitness.std() + 1e-12)
+        grads[0].copy_(vn.virtual_weight_gradient(fitness, seeds, w.shape, sigma, pop, offsets[0]))
+        grads[1].copy_(vn.virtual_bias_gradient(fitness, seeds, b.shape, sigma, pop, offsets[1]))
+        opt.step()
+        losses.append((vn.linear(f, w, b) - target).square().mean())
+    return losses
+
+
+def data(rows, n_in, n_out, device, seed=1):
+    gen = torch.Generator().manual_seed(seed)
+    x, a = torch.randn(rows, n_in, generator=gen), torch.randn(n_in, n_out, generator=gen) / n_in ** 0.5
+    return x.to(device).to(BF16), torch.sin(2.0 * (x @ a)).to(device)
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--steps", type=int, default=200)
+    ap.add_argument("--width", type=int, default=256)
+    ap.add_argument("--blocks", type=int, default=2)
+    ap.add_argument("--rows", type=int, default=1024)
+    ap.add_argument("--es-steps", type=int, default=50)
+    args = ap.parse_args(argv)
+    device = torch.device("cuda:0")
+    x, target = data(args.rows, 32, 10, device)
+    centre = Centre(32, args.width, args.blocks, 10, device)
+    # the first step eagerly, the others as replays of one captured step
+    losses = [float(centre.step(x, target))]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = centre.step(x, target)
+    for i in range(1, args.steps):
+        graph.replay()
+        if i % 50 == 0 or i == args.steps - 1:
+            losses.append(float(loss))
+            print(f"step {i}: loss {losses[-1]:.4f}", flush=True)
+    es = [float(v) for v in tune_head(centre, x, 0.5 * target + 0.25, args.es_steps)]
+    if es:
+        print(f"head after {len(es)} estimated gradients: loss {es[0]:.4f} -> {es[-1]:.4f}", flush=True)
+    return losses, es
+
+
+if __name__ == "__main__":
+    main()
