@@ -86,10 +86,11 @@ def test_linear_backward_validation(lib):
     for name in ("dy", "x", "w", "pre", "dx", "dw", "db", "ws"):
         assert backward(lib, **{name: ODD}) == E.VN_ERR_ALIGN
     f = lib.vn_linear_backward_workspace_size
-    st, need = size_of(f, E.VN_F32, E.VN_F32, 4, 64, 8, 2, 7)
+    st, need = size_of(f, E.VN_F32, E.VN_F32, 1000, 64, 8, 2, 7)
     assert st == E.VN_OK and need > 0
-    assert backward(lib, wsb=need - 1) == E.VN_ERR_SHAPE
-    assert backward(lib, ws=None, wsb=need) == E.VN_ERR_NULL
+    assert backward(lib, rows=1000, wsb=need - 1) == E.VN_ERR_SHAPE
+    assert backward(lib, rows=1000, ws=None, wsb=need) == E.VN_ERR_NULL
+    assert size_of(f, E.VN_F32, E.VN_F32, 4, 64, 8, 2, 7) == (E.VN_OK, 0)   # (one launch, nothing between)
     assert size_of(f, E.VN_F32, E.VN_F32, 4, 64, 8, 2, 8)[0] == E.VN_ERR_VALUE
     assert size_of(f, E.VN_F32, E.VN_F32, 4, 64, 8, 7, 7)[0] == E.VN_ERR_VALUE
     assert f(E.VN_F32, E.VN_F32, 4, 64, 8, 2, 7, None) == E.VN_ERR_NULL

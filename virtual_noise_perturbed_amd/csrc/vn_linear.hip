@@ -68,6 +68,20 @@ template <typename T, int C> __device__ __forceinline__ Few<T, C> load_few(const
   return f;
 }
 
+// dz = dy act'(pre).
+struct Slope {
+  const void* dy;
+  Elem dy_type;
+  const void* pre;       // or null: dz = dy
+  Elem type;             // of pre and dz
+  Act act;
+  int64_t rows, n;
+  void* dz;              // or null
+  float* sums;           // (ceil(rows / span), n), or null
+  int32_t span;          // rows of a workgroup, a multiple of 8
+  float* db;             // small_kernel: dz's column sums, or null
+};
+
 // ROWS rows of an operand's stage on their way from memory to LDS, in the
 // registers of 256 threads: UNITS units a thread.  A row-major operand's thread
 // takes a segment of UNITS rows; a k-major one's takes UNITS neighbouring rows
@@ -136,6 +150,60 @@ struct Staged {
     }
   }
 
+  // The stage at k of dz, every element checked: r counts dz's rows, k-major its
+  // columns, of which `sum` takes what this thread holds, unrounded.
+  __device__ __forceinline__ void load_slope(const Slope& z, int64_t r0, int64_t k, float (&sum)[UNITS]) {
+    const int tid = threadIdx.x;
+    float v[UNITS][8], pre[UNITS][8];   // (of k)
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[u][i] = pre[u][i] = 0.0f;
+    if constexpr (!K_MAJOR) {
+      const int64_t kk = k + tid % SEGS * 8;
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int64_t r = r0 + u * STRIDE + tid / SEGS;
+        if (r < z.rows) {
+          raw_values(load_raw<true>(z.dy, z.dy_type, r, kk, z.n), z.dy_type, v[u]);
+          if (z.pre != nullptr) raw_values(load_raw<true>(z.pre, z.type, r, kk, z.n), z.type, pre[u]);
+        }
+      }
+    } else {
+      const int64_t kk = k + tid / STRIDE * 8;
+      const int64_t c = r0 + tid % STRIDE * UNITS;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+          if (kk + i < z.rows && c + u < z.n) {
+            const int64_t at = (kk + i) * z.n + c + u;
+            v[u][i] = z.dy_type == Elem::f32 ? static_cast<const float*>(z.dy)[at]
+                                             : static_cast<float>(static_cast<const __bf16*>(z.dy)[at]);
+            if (z.pre != nullptr) pre[u][i] = static_cast<float>(static_cast<const T*>(z.pre)[at]);
+          }
+    }
+    if (z.pre != nullptr)
+      with_act(z.act, [&](auto act) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] *= act_slope<decltype(act)::value>(pre[u][i]);
+      });
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      if constexpr (!K_MAJOR) {
+        run[u] = make_run(v[u], static_cast<const T*>(nullptr));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sum[u] += v[u][i];
+          few[i].e[u] = static_cast<T>(v[u][i]);
+        }
+      }
+    }
+  }
+
   // Pair I of unit U as pairs of its planes.
   template <int U, int I>
   __device__ __forceinline__ void pair() {
@@ -175,6 +243,77 @@ struct Staged {
   }
 };
 
+// The outputs of a tile, out of the accumulators of its 4 waves.
+template <int TM, int TN>
+__device__ __forceinline__ void store_tile(const Product& g, uint4* smem, f32x16 (&acc)[TM / 64][TN / 64], int64_t m0,
+                                           int64_t n0, uint32_t split) {
+  constexpr int WM = TM / 2, WN = TN / 2, MB = WM / 32, NB = WN / 32;
+  constexpr int OUT_PITCH = WN + 4;   // floats: rows of 16-byte writes spread over the banks
+  const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
+  // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS of
+  // its own; one copy of the code for all of them.
+  __syncthreads();
+  float* out = reinterpret_cast<float*>(smem) + wave * 32 * OUT_PITCH;
+  constexpr int LANES = WN / 8, ROWS = 64 / LANES;   // lanes of a row, rows at a time
+  constexpr int TURNS = 32 / ROWS / 2;               // of a block, two runs a lane
+  const int64_t col = n0 + wn * WN + lane % LANES * 8;
+  const int64_t row0 = m0 + wm * WM + lane / LANES;
+  const Epilogue e = g.e;
+  float bias[8];
+  if (g.splits == 1) load_bias(e, col, g.n, bias);
+  auto epilogue = [&](auto checked_c) {
+    constexpr bool CHECKED = decltype(checked_c)::value;
+#pragma unroll 1
+    for (int p = 0; p < MB * TURNS; ++p) {
+      if (p % TURNS == 0) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        static_for<MB>([&](auto ac) {
+          constexpr int A = decltype(ac)::value;
+          if (p == A * TURNS) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(out + l32 * OUT_PITCH + b * 32 + q * 8 + lh * 4) =
+                    f32x4{acc[A][b][4 * q], acc[A][b][4 * q + 1], acc[A][b][4 * q + 2], acc[A][b][4 * q + 3]};
+            // (keeps the compiler from sinking the branches' common end, which would index the accumulators)
+            asm volatile("; block %0" ::"n"(A));
+          }
+        });
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+      float z[2][8];
+      int64_t row[2];
+      bool ok[2];
+      RawRun res[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        row[i] = row0 + (2 * p + i) * ROWS;
+        ok[i] = row[i] < g.m && col < g.n;
+        const int r = (2 * (p % TURNS) + i) * ROWS + lane / LANES;
+        __builtin_memcpy(z[i], __builtin_assume_aligned(out + r * OUT_PITCH + lane % LANES * 8, 16), 32);
+      }
+      if (g.splits > 1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (ok[i]) store_run(g.partial + (static_cast<int64_t>(split) * g.m + row[i]) * g.pitch, col, g.pitch, z[i]);
+      } else {
+        if (e.residual != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (!CHECKED || ok[i]) res[i] = load_raw<CHECKED>(e.residual, e.out_type, row[i], col, g.n);
+        }
+        finish<2, CHECKED>(e, row, ok, col, g.n, bias, res, z);
+      }
+    }
+  };
+  if (m0 + TM <= g.m && n0 + TN <= g.n) epilogue(std::false_type{});
+  else epilogue(std::true_type{});
+}
+
 // One tile of TM x TN outputs by 4 waves (2 x 2), over one split of k.  Two LDS
 // slots: while a stage is multiplied out of one, the next is split into its
 // planes and stored to the other, a pair of values after each MFMA or two, and
@@ -192,8 +331,7 @@ __device__ __forceinline__ void tile_body(const Product& g, uint4* smem) {
   constexpr int A_UNITS = PLANES * TM * SEGS, SLOT = A_UNITS + PLANES * TN * SEGS;
   constexpr int TERMS = PLANES == 3 ? 6 : 1, MFMAS = TERMS * MB * NB;   // a k-step
   constexpr int READS = PLANES * (MB + NB);
-  constexpr int OUT_PITCH = WN + 4;   // floats: rows of 16-byte writes spread over the banks
-  static_assert(4 * 32 * OUT_PITCH <= 2 * SLOT * 4);
+  static_assert(4 * 32 * (WN + 4) <= 2 * SLOT * 4);   // (store_tile)
   using SA = Staged<T, TM, A_K>;
   using SB = Staged<T, TN, B_K>;
   const int lane = threadIdx.x & 63;
@@ -331,66 +469,7 @@ __device__ __forceinline__ void tile_body(const Product& g, uint4* smem) {
   }
   static_assert(STEPS_K % 2 == 0);   // (a stage's first fragments are in buffer 0)
 
-  // Lane l holds row l % 32 of each 32-block and columns 8 * (v / 4) +
-  // 4 * (l / 32) + v % 4 for v < 16.  32 rows of a wave at a time pass through LDS of
-  // its own; one copy of the code for all of them.
-  __syncthreads();
-  float* out = reinterpret_cast<float*>(smem) + wave * 32 * OUT_PITCH;
-  constexpr int LANES = WN / 8, ROWS = 64 / LANES;   // lanes of a row, rows at a time
-  constexpr int TURNS = 32 / ROWS / 2;               // of a block, two runs a lane
-  const int64_t col = n0 + wn * WN + lane % LANES * 8;
-  const int64_t row0 = m0 + wm * WM + lane / LANES;
-  const Epilogue e = g.e;
-  float bias[8];
-  if (g.splits == 1) load_bias(e, col, g.n, bias);
-  auto epilogue = [&](auto checked_c) {
-    constexpr bool CHECKED = decltype(checked_c)::value;
-#pragma unroll 1
-    for (int p = 0; p < MB * TURNS; ++p) {
-      if (p % TURNS == 0) {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        static_for<MB>([&](auto ac) {
-          constexpr int A = decltype(ac)::value;
-          if (p == A * TURNS) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<f32x4*>(out + l32 * OUT_PITCH + b * 32 + q * 8 + lh * 4) =
-                    f32x4{acc[A][b][4 * q], acc[A][b][4 * q + 1], acc[A][b][4 * q + 2], acc[A][b][4 * q + 3]};
-            // (keeps the compiler from sinking the branches' common end, which would index the accumulators)
-            asm volatile("; block %0" ::"n"(A));
-          }
-        });
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      }
-      float z[2][8];
-      int64_t row[2];
-      bool ok[2];
-      RawRun res[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        row[i] = row0 + (2 * p + i) * ROWS;
-        ok[i] = row[i] < g.m && col < g.n;
-        const int r = (2 * (p % TURNS) + i) * ROWS + lane / LANES;
-        __builtin_memcpy(z[i], __builtin_assume_aligned(out + r * OUT_PITCH + lane % LANES * 8, 16), 32);
-      }
-      if (g.splits > 1) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (ok[i]) store_run(g.partial + (static_cast<int64_t>(split) * g.m + row[i]) * g.pitch, col, g.pitch, z[i]);
-      } else {
-        if (e.residual != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!CHECKED || ok[i]) res[i] = load_raw<CHECKED>(e.residual, e.out_type, row[i], col, g.n);
-        }
-        finish<2, CHECKED>(e, row, ok, col, g.n, bias, res, z);
-      }
-    }
-  };
-  if (m0 + TM <= g.m && n0 + TN <= g.n) epilogue(std::false_type{});
-  else epilogue(std::true_type{});
+  store_tile<TM, TN>(g, smem, acc, m0, n0, split);
 }
 
 template <typename T, int TM, int TN>
@@ -416,6 +495,84 @@ __global__ __launch_bounds__(256, (per_cu<T, TILE>())) void gradient_kernel(Prod
   const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
   if (g.a.k_major) tile_body<T, TILE, TILE, true, true>(g, smem);
   else tile_body<T, TILE, TILE, false, true>(g, smem);
+}
+
+// Gradients of a small layer in one launch: each tile forms the dz that it
+// multiplies, and the weight's first column of tiles sums it.  Stage by stage,
+// without the pipeline: there are few.
+template <typename T, bool A_K>
+__device__ __forceinline__ void small_body(const Product& g, const Slope& z, uint4* smem) {
+  constexpr int TILE = 64, BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES;
+  constexpr int A_UNITS = PLANES * TILE * SEGS;
+  using SA = Staged<T, TILE, A_K>;
+  using SB = Staged<T, TILE, true>;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+  const int wave = threadIdx.x >> 6;
+  const int wm = wave & 1, wn = wave >> 1;
+  const uint32_t id = blockIdx.x - g.first;
+  const int64_t m0 = static_cast<int64_t>(id / g.tiles_n) * TILE, n0 = static_cast<int64_t>(id % g.tiles_n) * TILE;
+  SA sa;
+  SB sb;
+  float sum[SA::UNITS] = {};
+  f32x16 acc[1][1] = {};
+  const uint4* a = smem + (wm * 32 + l32) * SEGS;
+  const uint4* b = smem + A_UNITS + (wn * 32 + l32) * SEGS;
+  const bool product = g.e.out != nullptr;   // (else the column sums alone)
+#pragma unroll 1
+  for (int64_t k = 0; k < g.k; k += BK) {
+    if (product) sb.load_checked(g.b, n0, g.n, k, g.k);
+    sa.load_slope(z, m0, k, sum);
+    if (!product) continue;
+    __syncthreads();   // the stage before is multiplied
+    static_for<SA::STEPS>([&](auto jc) { sa.template step<decltype(jc)::value>(smem); });
+    static_for<SB::STEPS>([&](auto jc) { sb.template step<decltype(jc)::value>(smem + A_UNITS); });
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < BK / 16; ++t) {
+      const int seg = (2 * t + lh) ^ swz<SEGS>(l32);
+      bf16x8 fa[PLANES], fb[PLANES];
+#pragma unroll
+      for (int q = 0; q < PLANES; ++q) {
+        fa[q] = __builtin_bit_cast(bf16x8, a[q * TILE * SEGS + seg]);
+        fb[q] = __builtin_bit_cast(bf16x8, b[q * TILE * SEGS + seg]);
+      }
+      auto multiply = [&](int p, int q) {
+        acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q], fa[p], acc[0][0], 0, 0, 0);
+      };
+      if constexpr (PLANES == 3) {   // smallest first
+        multiply(2, 0);
+        multiply(1, 1);
+        multiply(0, 2);
+        multiply(1, 0);
+        multiply(0, 1);
+      }
+      multiply(0, 0);
+    }
+  }
+  if (A_K && z.db != nullptr && n0 == 0) {
+    // the segments' sums of each column, in their order
+    float* s = reinterpret_cast<float*>(smem);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < SA::UNITS; ++u)
+      s[threadIdx.x / SA::STRIDE * TILE + threadIdx.x % SA::STRIDE * SA::UNITS + u] = sum[u];
+    __syncthreads();
+    if (threadIdx.x < TILE && m0 + threadIdx.x < g.m) {
+      float t = 0.0f;
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i) t += s[i * TILE + threadIdx.x];
+      z.db[m0 + threadIdx.x] = t;
+    }
+  }
+  if (product) store_tile<TILE, TILE>(g, smem, acc, m0, n0, 0);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void small_kernel(Products gs, Slope z) {
+  __shared__ uint4 smem[smem_units<T, 64, 64>()];
+  const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
+  if (g.a.k_major) small_body<T, true>(g, z, smem);
+  else small_body<T, false>(g, z, smem);
 }
 
 // ---- what follows a product ------------------------------------------------
@@ -482,18 +639,6 @@ __global__ __launch_bounds__(256) void join_kernel(Joins j) {
 
 // dz = dy act'(pre), as the products take it, and sums of its columns over `span`
 // rows each: 256 columns per workgroup, 8 a thread, 8 rows at a time.
-struct Slope {
-  const void* dy;
-  Elem dy_type;
-  const void* pre;       // or null: dz = dy
-  Elem type;             // of pre and dz
-  Act act;
-  int64_t rows, n;
-  void* dz;              // or null
-  float* sums;           // (ceil(rows / span), n), or null
-  int32_t span;          // rows of a workgroup, a multiple of 8
-};
-
 __global__ __launch_bounds__(256) void slope_kernel(Slope p) {
   __shared__ float s[8 * 256];
   const int seg = threadIdx.x & 31, group = threadIdx.x >> 5;
@@ -665,6 +810,14 @@ hipError_t linear_steps(const LinearParams& p, Arena& ws, hipStream_t stream) {
   return run_products(gs, tile, p.type, Joins{}, stream);
 }
 
+// Gradients in one launch, without a workspace: 12.6 us of a caller's time where three
+// launches take 20.5, and on the GPU 6.2 and 9.4 us at 5 x 95 x 14 (bf16).  Past these
+// sizes the stages, which are not pipelined, cost more than the launches: 20 and
+// 12 us at 256^3 (fp32), 45 and 15 us at 512 x 1000 x 512 (bf16).
+bool small_applies(const LinearBackwardParams& p) {
+  return p.rows > 0 && p.in > 0 && p.out > 0 && p.rows <= 128 && p.out <= 128 && p.in <= 2048;
+}
+
 hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need_dw, bool need_db, Arena& ws,
                           hipStream_t stream) {
   const bool run = ws.base != nullptr;
@@ -679,9 +832,10 @@ hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need
   int span = 64;
   while (span > 8 && (p.rows + span - 1) / span * ((p.out + 255) / 256) < 512) span /= 2;
   const int64_t parts = (p.rows + span - 1) / span;
-  Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr, span};
-  if (need_dz) z.dz = ws.take<char>(p.rows * p.out * size);
-  if (need_db) z.sums = ws.take<float>(parts * p.out * 4);
+  Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr, span, nullptr};
+  const bool small = small_applies(p);
+  if (need_dz && !small) z.dz = ws.take<char>(p.rows * p.out * size);
+  if (need_db && !small) z.sums = ws.take<float>(parts * p.out * 4);
   Products gs{};
   const void* dz = need_dz ? z.dz : p.dy;
   if (need_dx) {
@@ -701,6 +855,31 @@ hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need
     g.n = p.in;
     g.k = p.rows;
     g.e = {nullptr, nullptr, Act::none, p.dw_type, p.type, p.dw, nullptr};
+  }
+  if (small) {
+    if (need_db && !need_dw) {   // its tiles for the sums alone, which keep their order
+      Product& g = gs.g[gs.count++];
+      g.a = {dz, p.out, true};
+      g.b = {nullptr, 1, true};
+      g.m = p.out;
+      g.n = 1;
+      g.k = p.rows;
+      g.e.out = nullptr;
+    }
+    if (!run || gs.count == 0) return hipSuccess;
+    uint32_t first = 0;
+    for (int i = 0; i < gs.count; ++i) {
+      Product& g = gs.g[i];
+      g.splits = 1;
+      g.tiles_m = static_cast<int32_t>((g.m + 63) / 64);
+      g.tiles_n = static_cast<int32_t>((g.n + 63) / 64);
+      g.first = first;
+      first += static_cast<uint32_t>(g.tiles_m * g.tiles_n);
+    }
+    z.db = need_db ? p.db : nullptr;
+    if (p.type == Elem::f32) small_kernel<float><<<first, 256, 0, stream>>>(gs, z);
+    else small_kernel<__bf16><<<first, 256, 0, stream>>>(gs, z);
+    return hipGetLastError();
   }
   if (run && (need_dz || need_db) && parts > 0) {
     slope_kernel<<<static_cast<unsigned>(parts * ((p.out + 255) / 256)), 256, 0, stream>>>(z);
