@@ -313,12 +313,12 @@ int vn_noise_f32(const void* seeds, int32_t seed_dtype, int64_t pop, int64_t n, 
  *              the caller
  * VN_BF16: bf16 products, fp32 accumulation, one rounding to the outputs.
  * VN_F32: products of the operands split into three bf16 values each (what is
- * dropped is below 2^-24 of a product), fp32 accumulation; up to 16 rows
+ * dropped is below 2^-23 of a product), fp32 accumulation; up to 32 rows
  * multiply in fp32.  A non-finite fp32 input makes the outputs it reaches
  * non-finite (an infinity may come out as NaN).
  * in == 0 gives z = b.  Errors: VN_ERR_NULL, VN_ERR_SHAPE (negative size,
  * workspace too small), VN_ERR_VALUE (activation), VN_ERR_DTYPE,
- * VN_ERR_OVERFLOW (a size product, or 2^31 and more tiles of 64 x 64),
+ * VN_ERR_OVERFLOW (a size of 2^30 and more, or 2^31 tiles of 64 x 64),
  * VN_ERR_ALIGN (x, w or workspace not 16-byte aligned, another pointer not
  * aligned to its element).
  */

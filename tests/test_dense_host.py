@@ -37,6 +37,7 @@ def test_linear_validation(lib):
     for name in ("rows", "i", "o"):
         assert linear(lib, **{name: -1}) == E.VN_ERR_SHAPE
         assert linear(lib, **{name: 1 << 31}) == E.VN_ERR_OVERFLOW
+        assert linear(lib, **{name: 1 << 30}) == E.VN_ERR_OVERFLOW   # threads past 32 bits
     assert linear(lib, rows=(1 << 31) - 1, o=(1 << 31) - 1) == E.VN_ERR_OVERFLOW    # tiles past 31 bits
     assert linear(lib, act=5) == E.VN_ERR_VALUE
     assert linear(lib, act=-1) == E.VN_ERR_VALUE

@@ -43,12 +43,13 @@ bool act_of(int32_t activation, vn::Act* a) {
   }
 }
 
-// Sizes of a linear layer: the three matrices' bytes with three bf16 planes,
-// 64-padding and split partial sums in int64, and tile counts in 31 bits.
+// Sizes of a linear layer: each below 2^30 and each pair's tiles of 64 x 64 below
+// 2^31, so that every launch has fewer than 2^32 threads wherever the matrices fit
+// the GPU, and byte counts fit int64.
 int check_linear_sizes(int64_t rows, int64_t in, int64_t out) {
   if (rows < 0 || in < 0 || out < 0) return VN_ERR_SHAPE;
+  if (rows >= int64_t{1} << 30 || in >= int64_t{1} << 30 || out >= int64_t{1} << 30) return VN_ERR_OVERFLOW;
   constexpr int64_t kMost = int64_t{1} << 31;
-  if (rows >= kMost || in >= kMost || out >= kMost) return VN_ERR_OVERFLOW;
   const int64_t d[3] = {(rows + 63) / 64, (in + 63) / 64, (out + 63) / 64};
   for (int i = 0; i < 3; ++i)
     if (d[i] * d[(i + 1) % 3] >= kMost) return VN_ERR_OVERFLOW;

@@ -6,7 +6,7 @@
 //   - bf16 operands as they are;
 //   - fp32 operands as three bf16 values each, v = h + m + l (h = bf16(v),
 //     m = bf16(v - h), l = bf16(v - h - m): 24 bits and more), and the six
-//     products hh, hm, mh, hl, mm, lh; what is dropped is below 2^-24 of a
+//     products hh, hm, mh, hl, mm, lh; what is dropped is below 2^-23 of a
 //     product.  Six bf16 products at 16x the fp32 matrix rate take 0.4 of the
 //     fp32 matrix cores' time.
 // dz is rounded to bf16 for the products of bf16 operands; db is summed from
@@ -828,8 +828,10 @@ hipError_t backward_steps(const LinearBackwardParams& p, bool need_dx, bool need
   // dz is dy itself where that serves
   const bool plain = p.act == Act::none && p.dy_type == p.type;
   const bool need_dz = !plain && (need_dx || need_dw) && p.rows > 0 && p.out > 0;
-  // 64 rows a workgroup, or fewer where those would leave CUs idle
+  // 64 rows a workgroup, or fewer where those would leave CUs idle, or more where
+  // they would be too many for a launch
   int span = 64;
+  while ((p.rows + span - 1) / span * ((p.out + 255) / 256) > int64_t{1} << 23) span *= 2;
   while (span > 8 && (p.rows + span - 1) / span * ((p.out + 255) / 256) < 512) span /= 2;
   const int64_t parts = (p.rows + span - 1) / span;
   Slope z{p.dy, p.dy_type, p.act == Act::none ? nullptr : p.pre, p.type, p.act, p.rows, p.out, nullptr, nullptr, span, nullptr};

@@ -115,7 +115,10 @@ void launch_few_of(const Product& g, hipStream_t stream) {
 
 }  // namespace
 
-bool few_applies(const Product& g) { return g.m <= 32 && !g.a.k_major && !g.b.k_major; }
+bool few_applies(const Product& g) {
+  // (columns: a launch has fewer than 2^32 threads)
+  return g.m <= 32 && g.n <= int64_t{1} << 26 && !g.a.k_major && !g.b.k_major;
+}
 
 hipError_t launch_few(const Product& g, Elem type, hipStream_t stream) {
   if (type == Elem::f32) launch_few_of<float>(g, stream);
