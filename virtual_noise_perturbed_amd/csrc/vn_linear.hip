@@ -83,17 +83,17 @@ struct Slope {
 };
 
 // ROWS rows of an operand's stage on their way from memory to LDS, in the
-// registers of 256 threads: UNITS units a thread.  A row-major operand's thread
+// registers of THREADS threads: UNITS units each.  A row-major operand's thread
 // takes a segment of UNITS rows; a k-major one's takes UNITS neighbouring rows
 // (columns in memory) of one segment, 8 loads that it transposes in registers.
 // Rows past the end are read from the last row (k-major: from what follows in
 // memory, inside the matrix); they reach only outputs that are not stored.
 // k past the end is zero.
-template <typename T, int ROWS, bool K_MAJOR>
+template <typename T, int ROWS, bool K_MAJOR, int THREADS>
 struct Staged {
   static constexpr int PLANES = Kind<T>::PLANES, SEGS = Kind<T>::BK / 8;
-  static constexpr int UNITS = ROWS * SEGS / 256;
-  static constexpr int STRIDE = 256 / SEGS;   // threads side by side
+  static constexpr int UNITS = ROWS * SEGS / THREADS;
+  static constexpr int STRIDE = THREADS / SEGS;   // threads side by side
   static constexpr int STEPS = UNITS * 2;     // of the way to LDS: two pairs of k each
   Run8<T> run[K_MAJOR ? 1 : UNITS];
   Few<T, UNITS> few[K_MAJOR ? 8 : 1];
@@ -243,11 +243,11 @@ struct Staged {
   }
 };
 
-// The outputs of a tile, out of the accumulators of its 4 waves.
-template <int TM, int TN>
-__device__ __forceinline__ void store_tile(const Product& g, uint4* smem, f32x16 (&acc)[TM / 64][TN / 64], int64_t m0,
-                                           int64_t n0, uint32_t split) {
-  constexpr int WM = TM / 2, WN = TN / 2, MB = WM / 32, NB = WN / 32;
+// The outputs of a tile, out of the accumulators of its WAVES waves (2 rows of them).
+template <int TM, int TN, int WAVES>
+__device__ __forceinline__ void store_tile(const Product& g, uint4* smem, f32x16 (&acc)[TM / 64][TN / 16 / WAVES],
+                                           int64_t m0, int64_t n0, uint32_t split) {
+  constexpr int WM = TM / 2, WN = TN * 2 / WAVES, MB = WM / 32, NB = WN / 32;
   constexpr int OUT_PITCH = WN + 4;   // floats: rows of 16-byte writes spread over the banks
   const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -314,26 +314,28 @@ __device__ __forceinline__ void store_tile(const Product& g, uint4* smem, f32x16
   else epilogue(std::true_type{});
 }
 
-// One tile of TM x TN outputs by 4 waves (2 x 2), over one split of k.  Two LDS
+// One tile of TM x TN outputs by WAVES waves (2 rows of them), over one split of k.  Two LDS
 // slots: while a stage is multiplied out of one, the next is split into its
 // planes and stored to the other, a pair of values after each MFMA or two, and
 // the one after that is on its way into registers; one barrier a stage, before the
 // last k-step, whose MFMAs cover the next stage's first fragment reads.  (Split and
 // multiplied in turn, with the overlap left to two workgroups a CU, the two kept
 // step with each other and took the sum of both: 3570 cycles for a 128 x 128 x 32
-// stage in fp32 whose MFMAs take 1536.)
+// stage in fp32 whose MFMAs take 1536.)  2048^3 in fp32: 92 us, 187 TFLOP/s, with 8
+// waves, two a SIMD; 110 us with 4.  The MFMAs alone take 75 us: six times the
+// product's operations at 1.4 PFLOP/s, which is what the card sustains.
 // The matrix cores get B's rows first, so that a lane holds 4 neighbouring columns of
 // an output row; the outputs pass through LDS once more to leave in runs of 8.
-template <typename T, int TM, int TN, bool A_K, bool B_K>
+template <typename T, int TM, int TN, int WAVES, bool A_K, bool B_K>
 __device__ __forceinline__ void tile_body(const Product& g, uint4* smem) {
   constexpr int BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES, STEPS_K = BK / 16;
-  constexpr int WM = TM / 2, WN = TN / 2, MB = WM / 32, NB = WN / 32;
+  constexpr int WM = TM / 2, WN = TN * 2 / WAVES, MB = WM / 32, NB = WN / 32;
   constexpr int A_UNITS = PLANES * TM * SEGS, SLOT = A_UNITS + PLANES * TN * SEGS;
   constexpr int TERMS = PLANES == 3 ? 6 : 1, MFMAS = TERMS * MB * NB;   // a k-step
   constexpr int READS = PLANES * (MB + NB);
-  static_assert(4 * 32 * (WN + 4) <= 2 * SLOT * 4);   // (store_tile)
-  using SA = Staged<T, TM, A_K>;
-  using SB = Staged<T, TN, B_K>;
+  static_assert(WAVES * 32 * (WN + 4) <= 2 * SLOT * 4);   // (store_tile)
+  using SA = Staged<T, TM, A_K, 64 * WAVES>;
+  using SB = Staged<T, TN, B_K, 64 * WAVES>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
@@ -469,32 +471,229 @@ __device__ __forceinline__ void tile_body(const Product& g, uint4* smem) {
   }
   static_assert(STEPS_K % 2 == 0);   // (a stage's first fragments are in buffer 0)
 
-  store_tile<TM, TN>(g, smem, acc, m0, n0, split);
+  store_tile<TM, TN, WAVES>(g, smem, acc, m0, n0, split);
 }
 
 template <typename T, int TM, int TN>
 constexpr int smem_units() {
   return 2 * Kind<T>::PLANES * (TM + TN) * (Kind<T>::BK / 8);
 }
-template <typename T, int T_>
-constexpr int per_cu() {   // workgroups: LDS allows so many, and their registers
-  return T_ == 64 ? 3 : sizeof(T) == 4 ? 1 : 2;
+// Waves of a workgroup: fp32's large tiles have the LDS of a CU to themselves.
+template <typename T, int TILE>
+constexpr int waves_of() {
+  return TILE == 128 && sizeof(T) == 4 ? 8 : 4;
+}
+template <typename T, int TILE>
+constexpr int per_simd() {   // waves, as LDS and registers allow
+  return TILE == 64 ? 3 : 2;
 }
 
 // The forward's product.
 template <typename T, int TILE>
-__global__ __launch_bounds__(256, (per_cu<T, TILE>())) void tile_kernel(Product g) {
+__global__ __launch_bounds__((64 * waves_of<T, TILE>()), (per_simd<T, TILE>())) void tile_kernel(Product g) {
   __shared__ uint4 smem[smem_units<T, TILE, TILE>()];
-  tile_body<T, TILE, TILE, false, false>(g, smem);
+  tile_body<T, TILE, TILE, waves_of<T, TILE>(), false, false>(g, smem);
 }
 
 // The gradients' products, one or both.
 template <typename T, int TILE>
-__global__ __launch_bounds__(256, (per_cu<T, TILE>())) void gradient_kernel(Products gs) {
+__global__ __launch_bounds__((64 * waves_of<T, TILE>()), (per_simd<T, TILE>())) void gradient_kernel(Products gs) {
   __shared__ uint4 smem[smem_units<T, TILE, TILE>()];
   const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
-  if (g.a.k_major) tile_body<T, TILE, TILE, true, true>(g, smem);
-  else tile_body<T, TILE, TILE, false, true>(g, smem);
+  if (g.a.k_major) tile_body<T, TILE, TILE, waves_of<T, TILE>(), true, true>(g, smem);
+  else tile_body<T, TILE, TILE, waves_of<T, TILE>(), false, true>(g, smem);
+}
+
+// ---- fp32 tiles of 64 ------------------------------------------------------
+
+// An operand's stage of 64 rows in fp32, in the registers of 512 threads: 4 k of a
+// row each, half a unit.
+template <bool K_MAJOR>
+struct Quad {
+  static constexpr int SEGS = Kind<float>::BK / 8;
+  float v[4];
+
+  // This thread's row and first k of a stage.
+  static __device__ __forceinline__ int row() { return K_MAJOR ? threadIdx.x & 63 : threadIdx.x >> 3; }
+  static __device__ __forceinline__ int quad() { return K_MAJOR ? threadIdx.x >> 6 : threadIdx.x & 7; }
+
+  static __device__ __forceinline__ const float* at(const Operand& o, int64_t r0, int64_t rows) {
+    const int64_t r = r0 + row() < rows ? r0 + row() : rows - 1;
+    const float* p = static_cast<const float*>(o.p);
+    return K_MAJOR ? p + quad() * 4 * o.ld + r : p + r * o.ld + quad() * 4;
+  }
+  // The stage at k, all of whose k exist.
+  __device__ __forceinline__ void load(const Operand& o, const float* at, int64_t k) {
+    if constexpr (K_MAJOR) {
+      const float* p = at + k * o.ld;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p[i * o.ld];
+    } else {
+      u32x4_any u;
+      __builtin_memcpy(&u, at + k, 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_bit_cast(float, static_cast<uint32_t>(u[i]));
+    }
+  }
+  // The last, ragged stage: zeros past its end.
+  __device__ __forceinline__ void load_ragged(const Operand& o, const float* at, int64_t k, int64_t kn) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = k + quad() * 4 + i < kn ? at[K_MAJOR ? (k + i) * o.ld : k + i] : 0.0f;
+  }
+  // Its planes to the slot at `lds`.
+  __device__ __forceinline__ void store(uint4* lds) const {
+    uint32_t w[3][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) split_pair(v[2 * i], v[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+    const int r = row(), s = (quad() >> 1) ^ swz<SEGS>(r);
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      reinterpret_cast<uint2*>(lds + q * 64 * SEGS + r * SEGS + s)[quad() & 1] = make_uint2(w[q][0], w[q][1]);
+  }
+};
+
+// One tile of 64 x 64 outputs by 8 waves: 2 x 2 quarters, each by two waves that
+// take one of a stage's two k-steps and join their sums in the end, so that every
+// SIMD has two waves of one workgroup where tiles are few (1000^3: 20.0 us, 23.8
+// with 4 waves that take both k-steps).  What is left beside the products' 12 us
+// there are the loads, 5 us at 16 KB a stage from the L2, and the splitting, 3 us.  A stage: the barrier; then between its MFMAs the next stage's
+// fragments are read, the one after that goes from registers to the slot that this
+// one has left, and a load 6 stages ahead takes its registers.
+template <bool A_K, bool B_K>
+__device__ __forceinline__ void quad_body(const Product& g, uint4* smem) {
+  constexpr int BK = Kind<float>::BK, SEGS = BK / 8, A_UNITS = 3 * 64 * SEGS, SLOT = 2 * A_UNITS;
+  constexpr int RAWS = 4;   // stages in registers
+  using QA = Quad<A_K>;
+  using QB = Quad<B_K>;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2, wm = wave & 1, wn = (wave >> 1) & 1;
+  const uint32_t tiles = static_cast<uint32_t>(g.tiles_m) * g.tiles_n;
+  const uint32_t id = blockIdx.x - g.first, split = id / tiles;
+  uint32_t tm, tn;
+  tile_of(id - split * tiles, g.tiles_m, g.tiles_n, tm, tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * 64, n0 = static_cast<int64_t>(tn) * 64;
+  const int64_t stages = (g.k + BK - 1) / BK;
+  const int64_t per = (stages + g.splits - 1) / g.splits;
+  const int64_t begin = split * per * BK;
+  const int64_t end = (split + 1) * per * BK < g.k ? (split + 1) * per * BK : g.k;
+  const int64_t whole = begin < end ? begin + (end - begin) / BK * BK : begin;   // its last stage may be ragged
+
+  QA qa[RAWS];
+  QB qb[RAWS];
+  const float* const at_a = QA::at(g.a, m0, g.m);
+  const float* const at_b = QB::at(g.b, n0, g.n);
+  auto load = [&](int64_t k, auto rc) {
+    constexpr int R = decltype(rc)::value;
+    if (k >= whole) return;
+    qa[R].load(g.a, at_a, k);
+    qb[R].load(g.b, at_b, k);
+  };
+  uint4* const slots[2] = {smem, smem + SLOT};
+  const int seg = (2 * half + lh) ^ swz<SEGS>(l32);
+  const int arow = (wm * 32 + l32) * SEGS + seg, brow = A_UNITS + (wn * 32 + l32) * SEGS + seg;
+  bf16x8 fa[2][3], fb[2][3];
+  auto read = [&](const uint4* slot, auto bufc, int q) {
+    constexpr int BUF = decltype(bufc)::value;
+    if (q < 3) fa[BUF][q] = __builtin_bit_cast(bf16x8, slot[q * 64 * SEGS + arow]);
+    else fb[BUF][q - 3] = __builtin_bit_cast(bf16x8, slot[(q - 3) * 64 * SEGS + brow]);
+  };
+  f32x16 acc = {};
+  // Products of the planes, smallest first.
+  constexpr int kA[6] = {2, 1, 0, 1, 0, 0}, kB[6] = {0, 1, 2, 0, 1, 0};
+
+  if (begin < whole) {
+    static_for<RAWS>([&](auto rc) { load(begin + decltype(rc)::value * BK, rc); });
+    static_for<2>([&](auto rc) {   // (the second, where it does not exist, is stored and not used)
+      constexpr int R = decltype(rc)::value;
+      qa[R].store(slots[R]);
+      qb[R].store(slots[R] + A_UNITS);
+      load(begin + (RAWS + R) * BK, rc);
+    });
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 6; ++q) read(slots[0], std::integral_constant<int, 0>{}, q);
+  }
+  // The stage at k, number S modulo RAWS.
+  auto stage = [&](int64_t k, auto sc) {
+    constexpr int S = decltype(sc)::value, P = S & 1, R = (S + 2) % RAWS;
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();   // the next stage is whole; this one's fragments are in registers
+    static_for<6>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[P][kB[m]], fa[P][kA[m]], acc, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      read(slots[P ^ 1], std::integral_constant<int, P ^ 1>{}, m);
+      if constexpr (m == 1) qa[R].store(slots[P]);
+      if constexpr (m == 3) qb[R].store(slots[P] + A_UNITS);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    load(k + (2 + RAWS) * BK, std::integral_constant<int, R>{});
+  };
+  for (int64_t k = begin; k < whole; k += RAWS * BK)
+    static_for<RAWS>([&](auto sc) {
+      if (k + decltype(sc)::value * BK < whole) stage(k + decltype(sc)::value * BK, sc);
+    });
+  if (whole < end) {
+    qa[0].load_ragged(g.a, at_a, whole, end);
+    qb[0].load_ragged(g.b, at_b, whole, end);
+    __syncthreads();
+    qa[0].store(slots[0]);
+    qb[0].store(slots[0] + A_UNITS);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 6; ++q) read(slots[0], std::integral_constant<int, 0>{}, q);
+    static_for<6>([&](auto mc) {
+      constexpr int m = decltype(mc)::value;
+      acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[0][kB[m]], fa[0][kA[m]], acc, 0, 0, 0);
+    });
+  }
+
+  // Lane l holds row l % 32 of its quarter and columns 8 * (v / 4) + 4 * (l / 32) +
+  // v % 4 for v < 16.  The halves' sums meet in LDS, the first's first.
+  constexpr int OUT_PITCH = 36;
+  float* out = reinterpret_cast<float*>(smem) + (wave & 3) * 32 * OUT_PITCH;
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (half == h) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4& to = *reinterpret_cast<f32x4*>(out + l32 * OUT_PITCH + q * 8 + lh * 4);
+        const f32x4 mine = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+        if (h == 0) to = mine;
+        else to = to + mine;
+      }
+    }
+    __syncthreads();
+  }
+  const int r = half * 16 + lane / 4, c = lane % 4 * 8;
+  const int64_t row = m0 + wm * 32 + r, col = n0 + wn * 32 + c;
+  if (row >= g.m || col >= g.n) return;
+  float z[1][8];
+  __builtin_memcpy(z[0], __builtin_assume_aligned(out + r * OUT_PITCH + c, 16), 32);
+  if (g.splits > 1) {
+    store_run(g.partial + (static_cast<int64_t>(split) * g.m + row) * g.pitch, col, g.pitch, z[0]);
+    return;
+  }
+  float bias[8];
+  RawRun res[1];
+  load_bias(g.e, col, g.n, bias);
+  if (g.e.residual != nullptr) res[0] = load_raw<true>(g.e.residual, g.e.out_type, row, col, g.n);
+  finish<1, true>(g.e, {row}, {true}, col, g.n, bias, res, z);
+}
+
+__global__ __launch_bounds__(512, 4) void quad_kernel(Product g) {
+  __shared__ uint4 smem[smem_units<float, 64, 64>()];
+  quad_body<false, false>(g, smem);
+}
+
+__global__ __launch_bounds__(512, 4) void quad_gradient_kernel(Products gs) {
+  __shared__ uint4 smem[smem_units<float, 64, 64>()];
+  const Product& g = gs.g[gs.count > 1 && blockIdx.x >= gs.g[1].first ? 1 : 0];
+  if (g.a.k_major) quad_body<true, true>(g, smem);
+  else quad_body<false, true>(g, smem);
 }
 
 // Gradients of a small layer in one launch: each tile forms the dz that it
@@ -504,8 +703,8 @@ template <typename T, bool A_K>
 __device__ __forceinline__ void small_body(const Product& g, const Slope& z, uint4* smem) {
   constexpr int TILE = 64, BK = Kind<T>::BK, SEGS = BK / 8, PLANES = Kind<T>::PLANES;
   constexpr int A_UNITS = PLANES * TILE * SEGS;
-  using SA = Staged<T, TILE, A_K>;
-  using SB = Staged<T, TILE, true>;
+  using SA = Staged<T, TILE, A_K, 256>;
+  using SB = Staged<T, TILE, true, 256>;
   const int lane = threadIdx.x & 63, l32 = lane & 31, lh = lane >> 5;
   const int wave = threadIdx.x >> 6;
   const int wm = wave & 1, wn = wave >> 1;
@@ -564,7 +763,7 @@ __device__ __forceinline__ void small_body(const Product& g, const Slope& z, uin
       z.db[m0 + threadIdx.x] = t;
     }
   }
-  if (product) store_tile<TILE, TILE>(g, smem, acc, m0, n0, 0);
+  if (product) store_tile<TILE, TILE, 4>(g, smem, acc, m0, n0, 0);
 }
 
 template <typename T>
@@ -628,12 +827,20 @@ __global__ __launch_bounds__(256) void join_kernel(Joins j) {
   RawRun res[1];
   load_bias(g.e, c, g.n, bias);
   if (g.e.residual != nullptr) res[0] = load_raw<true>(g.e.residual, g.e.out_type, m, c, g.n);
-  for (int s = 0; s < g.splits; ++s) {
+  auto part = [&](int s) { return load_run(g.partial + (s * g.m + m) * g.pitch, c, g.pitch); };
+  auto add = [&](const Run8<float>& r) {
     float v[8];
-    run_values(load_run(g.partial + (s * g.m + m) * g.pitch, c, g.pitch), v);
+    run_values(r, v);
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[0][e] += v[e];
+  };
+  int s = 0;
+  for (; s + 4 <= g.splits; s += 4) {   // (4 on their way at a time)
+    const Run8<float> r[4] = {part(s), part(s + 1), part(s + 2), part(s + 3)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add(r[i]);
   }
+  for (; s < g.splits; ++s) add(part(s));
   finish<1, true>(g.e, {m}, {true}, c, g.n, bias, res, z);
 }
 
@@ -695,28 +902,73 @@ int64_t tiles_of(const Product& g, int tile) {
   return ((g.m + tile - 1) / tile) * ((g.n + tile - 1) / tile);
 }
 
-// The tile's side and the splits of the products of one launch.
+// The splits of k of the products of one launch on tiles of side `tile`, and what
+// the launch is expected to take, in us: the CUs take its workgroups in order, the
+// longer ones first, so that the last to end is a long one or the total and a short
+// one; a split product also writes and reads its partial sums, at 4 TB/s, and
+// joins them in another launch, 4 us and 0.15 for each split.  A stage of a tile takes a
+// CU `us`.
+double split_for(const Products& gs, int tile, int bk, double us, int (&splits)[2]) {
+  int64_t stages[2] = {1, 1}, tiles[2] = {0, 0}, total = 0;
+  for (int i = 0; i < gs.count; ++i) {
+    if (gs.g[i].k > bk) stages[i] = (gs.g[i].k + bk - 1) / bk;
+    tiles[i] = tiles_of(gs.g[i], tile);
+    total += tiles[i] * stages[i];
+  }
+  double best = -1.0;
+  for (int c = 0; c <= 4; ++c) {   // no splits; shares of 1, 1/2, 1/3, 1/4 of each CU's part
+    const int64_t share = c == 0 ? total : total / (256 * c) < 3 ? 3 : total / (256 * c);
+    int s[2] = {1, 1};
+    int64_t length[2] = {0, 0}, count[2] = {0, 0};
+    double joins = 0.0;
+    for (int i = 0; i < gs.count; ++i) {
+      const int64_t n = (stages[i] + share / 2) / share;
+      s[i] = static_cast<int>(n < 1 ? 1 : n);
+      length[i] = (stages[i] + s[i] - 1) / s[i];
+      count[i] = tiles[i] * s[i];
+      if (s[i] > 1)
+        joins += static_cast<double>(s[i]) * static_cast<double>(gs.g[i].m) * static_cast<double>(gs.g[i].n) * 8.0 / 4e6;
+    }
+    const bool joined = s[0] > 1 || s[1] > 1;
+    const int l = length[1] > length[0] ? 1 : 0;   // the longer
+    const double alone = static_cast<double>((count[l] + 255) / 256 * length[l]);
+    // (in one round, or with one length, `alone` says it all)
+    const double shared = gs.count > 1 && count[0] + count[1] > 256
+                              ? static_cast<double>(total) / 256.0 + static_cast<double>(length[1 - l]) : 0.0;
+    const double cost = us * (alone > shared ? alone : shared) + joins +
+                        (joined ? 4.0 + 0.15 * (s[0] > s[1] ? s[0] : s[1]) : 0.0);
+    if (best < 0.0 || cost < best) {
+      best = cost;
+      splits[0] = s[0];
+      splits[1] = s[1];
+    }
+  }
+  return best;
+}
+
+// The tile's side and the splits of the products of one launch.  What a stage of a
+// tile of 64 and of 128 takes a CU, measured: fp32 (32 of k) 0.5 and 1.3 us, bf16 (64
+// of k) 0.3 and 0.77.  For instance, on the GPU: fp32, 2048^3 takes 92 us on tiles of
+// 128 and 125 on 64, 1000^3 26.5 and 20; 2011 x 784 x 256 17.4 us whole and 16.3 in 2
+// splits; 777 x 1024 x 1000's gradients 54 us whole and 41.5 in 2 splits, 47.5 in 3.
+// bf16, 1000^3: 10.1 us whole, 16.8 in 2 splits.
 int plan(Products& gs, Elem type, Arena& ws) {
-  const int bk = type == Elem::f32 ? 32 : 64;
-  int64_t work[2] = {0, 0};   // stages of all tiles of 64, of 128
-  for (int i = 0; i < gs.count; ++i)
-    for (int t = 0; t < 2; ++t) work[t] += tiles_of(gs.g[i], 64 << t) * ((gs.g[i].k + bk - 1) / bk);
-  // Tiles of 128 where each CU gets 32 of their stages: 2048^3 in fp32 takes
-  // 113 us on them, 144 on tiles of 64; 4000 x 700 x 700 41 and 36 us.
-  const int tile = work[1] >= 256 * 32 ? 128 : 64;
-  // A workgroup's stages: an equal share of all for each CU (with two products, half
-  // of it, as theirs differ), but enough to repay a split's partial sums and their
-  // join.  fp32, 2011 x 784 x 256: 20.5 us whole, 17.4 in 2 splits, 18.3 in 4;
-  // 200 x 300 x 100: 10.2 whole, 9.2 in 3.  bf16, 1000^3: 10.1 whole, 16.8 in 2.
-  const int64_t least = type == Elem::f32 ? 3 : 8;
-  const int64_t each = gs.count > 0 ? work[tile / 128] / (256 * gs.count) : 0;
-  const int64_t share = each < least ? least : each;
+  if (gs.count == 0) return 64;
+  const bool f32 = type == Elem::f32;
+  int splits[2][2] = {};
+  const double small = split_for(gs, 64, f32 ? 32 : 64, f32 ? 0.5 : 0.3, splits[0]);
+  const double large = split_for(gs, 128, f32 ? 32 : 64, f32 ? 1.3 : 0.77, splits[1]);
+  const int tile = large < small ? 128 : 64;
+  for (int i = 0; i < gs.count; ++i) gs.g[i].splits = splits[tile / 128][i];
+  // the product with the longer workgroups first
+  if (gs.count > 1 && gs.g[1].k * gs.g[0].splits > gs.g[0].k * gs.g[1].splits) {
+    const Product g = gs.g[0];
+    gs.g[0] = gs.g[1];
+    gs.g[1] = g;
+  }
   uint32_t first = 0;
   for (int i = 0; i < gs.count; ++i) {
     Product& g = gs.g[i];
-    const int64_t stages = (g.k + bk - 1) / bk;
-    const int64_t s = stages / share;
-    g.splits = static_cast<int>(s < 1 ? 1 : s);
     g.tiles_m = static_cast<int32_t>((g.m + tile - 1) / tile);
     g.tiles_n = static_cast<int32_t>((g.n + tile - 1) / tile);
     g.first = first;
@@ -729,11 +981,16 @@ int plan(Products& gs, Elem type, Arena& ws) {
 
 template <typename T>
 void launch_tiles(const Products& gs, int tile, unsigned blocks, hipStream_t stream) {
-  if (!gs.g[0].b.k_major) {
-    if (tile == 128) tile_kernel<T, 128><<<blocks, 256, 0, stream>>>(gs.g[0]);
-    else tile_kernel<T, 64><<<blocks, 256, 0, stream>>>(gs.g[0]);
+  const bool forward = !gs.g[0].b.k_major;
+  if (tile == 128) {
+    constexpr int THREADS = 64 * waves_of<T, 128>();
+    if (forward) tile_kernel<T, 128><<<blocks, THREADS, 0, stream>>>(gs.g[0]);
+    else gradient_kernel<T, 128><<<blocks, THREADS, 0, stream>>>(gs);
+  } else if constexpr (sizeof(T) == 4) {
+    if (forward) quad_kernel<<<blocks, 512, 0, stream>>>(gs.g[0]);
+    else quad_gradient_kernel<<<blocks, 512, 0, stream>>>(gs);
   } else {
-    if (tile == 128) gradient_kernel<T, 128><<<blocks, 256, 0, stream>>>(gs);
+    if (forward) tile_kernel<T, 64><<<blocks, 256, 0, stream>>>(gs.g[0]);
     else gradient_kernel<T, 64><<<blocks, 256, 0, stream>>>(gs);
   }
 }
