@@ -66,7 +66,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
     any kernel spills to scratch memory (per-lane stack traffic in the hot
     loops is never intended here)."""
     out_tmp = LIB + ".tmp"
-    cmd = [hipcc(), *HIPCC_FLAGS, RESOURCE_REMARKS, *(extra_flags or []), "-shared", "-I", INCLUDE, "-I", CSRC,
+    cmd = [hipcc(), *HIPCC_FLAGS, RESOURCE_REMARKS, "-parallel-jobs=8", *(extra_flags or []), "-shared", "-I", INCLUDE, "-I", CSRC,
            *[os.path.join(CSRC, s) for s in SOURCES], "-o", out_tmp]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -22,8 +22,10 @@
 // never rounds to zero, so no denominator collapses to eps.
 //
 // What bounds it: 28 bytes per element with fp32 states and gradients, 16.03
-// with 8-bit states.  16 lanes x 8 elements hold one block of 128, so its
-// largest values are found within a row of 16 lanes.
+// with 8-bit states.  67 million elements: 361 us with fp32 states, bf16 gradients and
+// a bf16 copy, 206 us with 8-bit states and fp32 gradients (both 5.2 TB/s).
+// 16 lanes x 8 elements hold one block of 128, so its largest values are found
+// within a row of 16 lanes.
 #include "vn_dense.hpp"
 #include "vn_rows.hpp"
 

@@ -14,7 +14,9 @@
 // the lanes keep their columns from row to row, so the weights are loaded once
 // per workgroup and a backward pass's column sums stay in registers until the
 // workgroup has walked all its rows (blockIdx.x, + gridDim.x, ...).  The next
-// row's loads are issued before the current row's sums are formed.
+// row's loads are issued before the current row's sums are formed.  32768 x 4096 in
+// bf16: 103 us forward (5.2 TB/s) and 142 us backward with the join (5.6 TB/s), where
+// a copy of 1 GiB runs at 5.05 TB/s.
 #include <type_traits>
 
 #include "vn_dense.hpp"
