@@ -556,11 +556,12 @@ struct Quad {
 // One tile of 64 x 64 outputs by 8 waves: 2 x 2 quarters, each by two waves that
 // take one of a stage's two k-steps and join their sums in the end, so that every
 // SIMD has two waves of one workgroup where tiles are few (1000^3: 20.0 us, 23.8
-// with 4 waves that take both k-steps).  What bounds it then is what a CU
-// takes in: 16 KB a stage in 0.45 to 0.5 us, whatever the waves (two such groups a
-// workgroup with the stages in turn: the same time; loads left out: 5 us less there).  A stage: the barrier; then between its MFMAs the next stage's
-// fragments are read, the one after that goes from registers to the slot that this
-// one has left, and a load 6 stages ahead takes its registers.
+// with 4 waves that take both k-steps).  What bounds it then is what a CU takes in:
+// 16 KB a stage in 0.45 to 0.5 us, whatever the waves (two such groups a workgroup
+// with the stages in turn: the same time; loads left out: 5 us less there).
+// A stage: the barrier; then between its MFMAs the next stage's fragments are read,
+// the one after that goes from registers to the slot that this one has left, and a
+// load 6 stages ahead takes its registers.
 template <bool A_K, bool B_K>
 __device__ __forceinline__ void quad_body(const Product& g, uint4* smem) {
   constexpr int BK = Kind<float>::BK, SEGS = BK / 8, A_UNITS = 3 * 64 * SEGS, SLOT = 2 * A_UNITS;
